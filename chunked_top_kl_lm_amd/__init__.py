@@ -1,7 +1,8 @@
 """MI355X fused chunked top-K KL distillation loss: thin Python binding.
 
 The computation runs entirely in the HIP library libkdtopk.so (C ABI in
-include/kd_topk_kl.h).  This module only marshals arguments: PyTorch supplies
+include/kd_topk_kl.h; the operators around the head, in head_ops.py, in
+include/kd_head_ops.h).  This module only marshals arguments: PyTorch supplies
 device memory (torch.empty) and the current stream.  If the library is not
 built, every entry point raises; there is no fallback.
 """
@@ -10,11 +11,15 @@ from __future__ import annotations
 import ctypes
 import os
 
+from . import head_ops
+from .head_ops import (ACT8_BLOCK, act8_dequantize, act8_quantize, head_logits, head_logits_workspace_bytes, layer_norm,
+                       layer_norm_bwd, layer_norm_fwd, sample, sample_workspace_bytes)
+
 __all__ = ["KD_BF16", "KD_F32", "KD_NUM_PHASES", "PHASES", "KD_CACHE_PHASES", "CACHE_PHASES", "KdError", "lib", "workspace_bytes", "fwd_bwd",
            "fwd", "bwd", "fwd_workspace_bytes", "bwd_workspace_bytes", "dw_chunks", "KdTopKKLFunction",
            "kd_topk_kl_loss", "topk_cache", "mfma_probe", "topk_cache_workspace_bytes",
            "fwd_bwd_noalloc", "NOALLOC_SCRATCH_BYTES",
-           "status_str", "STATUS"]
+           "status_str", "STATUS", *head_ops.__all__]
 
 KD_BF16 = 0
 KD_F32 = 1
@@ -25,7 +30,8 @@ PHASES = ("chunk_prep", "gemm_fwd_lse", "kl_rows", "gemm_bwd_grad", "teacher_p",
           "gemm_dhidden", "dhidden_reduce", "gemm_dW")
 STATUS = {0: "KD_OK", 1: "KD_ERR_NULL_ARG", 2: "KD_ERR_BAD_SHAPE", 3: "KD_ERR_BAD_TAU",
           4: "KD_ERR_BAD_CHUNK", 5: "KD_ERR_DTYPE", 6: "KD_ERR_WORKSPACE",
-          7: "KD_ERR_BAD_INDEX", 8: "KD_ERR_HIP", 9: "KD_ERR_NOALLOC_SIZE"}
+          7: "KD_ERR_BAD_INDEX", 8: "KD_ERR_HIP", 9: "KD_ERR_NOALLOC_SIZE",
+          10: "KD_ERR_BAD_PARAM"}
 NOALLOC_SCRATCH_BYTES = 256 << 20     # KD_NOALLOC_SCRATCH_BYTES
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkdtopk.so")
@@ -81,6 +87,7 @@ def lib() -> ctypes.CDLL:
         L.kd_topk_cache_build_timed.restype = i32
         L.kd_mfma_probe.argtypes = [i32, i32, i32, vp, vp]
         L.kd_mfma_probe.restype = i32
+        head_ops.declare(L)
         L.kd_status_str.argtypes = [i32]
         L.kd_status_str.restype = ctypes.c_char_p
         _lib = L
@@ -148,9 +155,16 @@ def _check_workspace(workspace, status):
 
 def _check_inputs(hidden, W, teacher_idx, teacher_logit, mask):
     import torch
-    if not hidden.is_cuda:
-        raise ValueError("hidden must be a CUDA tensor")
-    _check_device(hidden.device, W=W, teacher_idx=teacher_idx, teacher_logit=teacher_logit, mask=mask)
+    if isinstance(hidden, (tuple, list)):
+        # the backward from an 8-bit checkpoint: W's dtype is the call's
+        q, _, T, d = head_ops.check_act8(hidden)
+        dev = q.device
+        hidden = torch.empty((T, d), dtype=W.dtype, device="meta")
+    else:
+        if not hidden.is_cuda:
+            raise ValueError("hidden must be a CUDA tensor")
+        dev = hidden.device
+    _check_device(dev, W=W, teacher_idx=teacher_idx, teacher_logit=teacher_logit, mask=mask)
     if hidden.dim() != 2 or W.dim() != 2 or teacher_idx.dim() != 2:
         raise ValueError("shapes: hidden [T,d], W [V,d], teacher_idx and teacher_logit [T,K]")
     T, d = hidden.shape
@@ -360,6 +374,10 @@ def bwd(hidden, W, teacher_idx, teacher_logit, mask, row_lse, tau: float = 1.0, 
         workspace=None, status=None, events=None):
     """Backward only (kd_topk_kl_bwd): gradients of grad_loss * loss.
 
+    hidden: the forward's, or its 8-bit checkpoint (q, scale) from
+    act8_quantize, whose values (rounded to W's dtype) then stand for it
+    (kd_topk_kl_bwd_act8; no `events`).
+
     grad_loss: 0-d float32 CUDA tensor or None (= 1).  grad_hidden:
     "float32", "bfloat16" or None (not computed).  grad_W: True (a new fp32
     [V,d] tensor), False (not computed); accumulate_into: an fp32 [V,d] CUDA
@@ -369,7 +387,10 @@ def bwd(hidden, W, teacher_idx, teacher_logit, mask, row_lse, tau: float = 1.0, 
     `events`: as for fwd_bwd (kd_topk_kl_bwd_timed)."""
     import torch
     T, d, V, K, dt = _check_inputs(hidden, W, teacher_idx, teacher_logit, mask)
-    dev = hidden.device
+    dev = W.device
+    act8 = tuple(hidden) if isinstance(hidden, (tuple, list)) else None
+    if act8 and events is not None:
+        raise ValueError("events: not with an 8-bit checkpoint")
     _check_device(dev, row_lse=row_lse, grad_loss=grad_loss, accumulate_into=accumulate_into,
                   workspace=workspace, status=status)
     _check_workspace(workspace, status)
@@ -390,16 +411,22 @@ def bwd(hidden, W, teacher_idx, teacher_logit, mask, row_lse, tau: float = 1.0, 
     else:
         gW, acc = (torch.empty((V, d), dtype=torch.float32, device=dev) if grad_W else None), 0
     gWb = torch.empty((V, d), dtype=torch.bfloat16, device=dev) if (grad_W_bf16 and gW is not None) else None
-    nbytes = bwd_workspace_bytes(T, d, V, K, chunk, dt)
+    if act8:
+        nbytes = int(lib().kd_topk_kl_bwd_act8_workspace_bytes(T, d, V, K, chunk, dt))
+    else:
+        nbytes = bwd_workspace_bytes(T, d, V, K, chunk, dt)
     if nbytes == 0:
         raise KdError(2)
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     stream = torch.cuda.current_stream(dev).cuda_stream
-    args = (_ptr(hidden), _ptr(W), dt, _ptr(teacher_idx), _ptr(teacher_logit), _ptr(mask), T, d, V, K,
+    rows = (_ptr(act8[0]), _ptr(act8[1])) if act8 else (_ptr(hidden),)
+    args = (*rows, _ptr(W), dt, _ptr(teacher_idx), _ptr(teacher_logit), _ptr(mask), T, d, V, K,
             float(tau), int(chunk), _ptr(row_lse), _ptr(grad_loss), _ptr(gH), gh_code, _ptr(gW), acc, _ptr(gWb),
             _ptr(workspace), workspace.numel(), _ptr(status), ctypes.c_void_p(stream))
-    if events is None:
+    if act8:
+        rc = lib().kd_topk_kl_bwd_act8(*args)
+    elif events is None:
         rc = lib().kd_topk_kl_bwd(*args)
     else:
         rc = lib().kd_topk_kl_bwd_timed(*args, _loss_events(events, T, chunk))
@@ -420,23 +447,31 @@ def _autograd_function():
         chunk's logits.  The hidden gradient comes back in hidden's dtype.
         The head gradient: with a grad_W_accumulator (fp32 [V,d], e.g. a
         master-weight gradient buffer) it is added there in fp32 and W gets
-        no .grad; otherwise it is returned in W's dtype."""
+        no .grad; otherwise it is returned in W's dtype.
+
+        checkpoint="int8" keeps hidden for the backward as its 8-bit
+        checkpoint (act8_quantize) instead: the loss is that of hidden, the
+        gradients are formed from the values the checkpoint stands for."""
 
         @staticmethod
-        def forward(ctx, hidden, W, teacher_idx, teacher_logit, mask, tau, chunk, grad_W_accumulator):
+        def forward(ctx, hidden, W, teacher_idx, teacher_logit, mask, tau, chunk, grad_W_accumulator,
+                    checkpoint=None):
+            head_ops._check_kind(checkpoint)
             loss, row_lse = fwd(hidden, W, teacher_idx, teacher_logit, mask, tau, chunk)
-            ctx.save_for_backward(hidden, W, teacher_idx, teacher_logit, mask, row_lse)
+            kept = (hidden,) if checkpoint is None else act8_quantize(hidden)
+            ctx.save_for_backward(W, teacher_idx, teacher_logit, mask, row_lse, *kept)
             ctx.tau, ctx.chunk, ctx.acc = tau, chunk, grad_W_accumulator
             return loss
 
         @staticmethod
         def backward(ctx, grad_loss):
-            hidden, W, teacher_idx, teacher_logit, mask, row_lse = ctx.saved_tensors
+            W, teacher_idx, teacher_logit, mask, row_lse, *kept = ctx.saved_tensors
+            hidden = kept[0] if len(kept) == 1 else tuple(kept)
             need_h, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
             if not (need_h or need_w):
-                return (None,) * 8
+                return (None,) * 9
             g = grad_loss.reshape(()).to(torch.float32).contiguous()
-            gh_kind = ("bfloat16" if hidden.dtype == torch.bfloat16 else "float32") if need_h else None
+            gh_kind = ("bfloat16" if W.dtype == torch.bfloat16 else "float32") if need_h else None
             use_acc = need_w and ctx.acc is not None
             gH, gW, gWb = bwd(hidden, W, teacher_idx, teacher_logit, mask, row_lse, ctx.tau, ctx.chunk,
                               grad_loss=g, grad_hidden=gh_kind, grad_W=need_w and not use_acc,
@@ -446,7 +481,7 @@ def _autograd_function():
                 dW = None
             else:
                 dW = gWb if W.dtype == torch.bfloat16 else gW
-            return gH, dW, None, None, None, None, None, None
+            return gH, dW, None, None, None, None, None, None, None
 
     return KdTopKKLFunction
 
@@ -460,15 +495,18 @@ def __getattr__(name):
         if _FN is None:
             _FN = _autograd_function()
         return _FN
+    if name == "KdLayerNormFunction":
+        return head_ops.KdLayerNormFunction
     raise AttributeError(name)
 
 
 def kd_topk_kl_loss(hidden, W, teacher_idx, teacher_logit, mask=None, tau: float = 1.0, chunk: int = 2048,
-                    grad_W_accumulator=None):
+                    grad_W_accumulator=None, checkpoint=None):
     """Differentiable loss: tau^2 * masked mean over positions of
     KL(teacher top-K softmax || student full-vocabulary softmax), computed
-    and differentiated by the HIP library."""
+    and differentiated by the HIP library.  checkpoint="int8" keeps hidden
+    for the backward pass in 8 bits (see KdTopKKLFunction)."""
     global _FN
     if _FN is None:
         _FN = _autograd_function()
-    return _FN.apply(hidden, W, teacher_idx, teacher_logit, mask, tau, chunk, grad_W_accumulator)
+    return _FN.apply(hidden, W, teacher_idx, teacher_logit, mask, tau, chunk, grad_W_accumulator, checkpoint)

@@ -1,18 +1,20 @@
-"""Build libkdtopk.so (the HIP library behind include/kd_topk_kl.h) for gfx950."""
+"""Build libkdtopk.so (the HIP library behind include/kd_topk_kl.h and
+kd_head_ops.h) for gfx950."""
 from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "kd_topk_kl.hip")
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("kd_topk_kl.hip", "kd_head_ops.hip")]
 LIB = os.path.join(PKG, "libkdtopk.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # no packed-fp32 VALU forms in device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(ROOT, "include"),
@@ -22,12 +24,21 @@ FLAGS = [
 def build(verbose: bool = False) -> str:
     """Compile the library in-tree; returns its path.  Raises on failure."""
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, SRC, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + r.stderr[-4000:])
+    with tempfile.TemporaryDirectory() as tmpdir:
+        objs = [os.path.join(tmpdir, os.path.basename(src) + ".o") for src in SOURCES]
+        cmds = [[HIPCC, *FLAGS, "-c", src, "-o", obj] for src, obj in zip(SOURCES, objs)]
+        procs = [subprocess.Popen(c, stdout=subprocess.DEVNULL, stderr=subprocess.PIPE, text=True) for c in cmds]
+        errs = [p.communicate()[1] for p in procs]
+        for p, err in zip(procs, errs):
+            if p.returncode != 0:
+                raise RuntimeError("hipcc failed:\n" + err[-4000:])
+        link = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
+        r = subprocess.run(link, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + r.stderr[-4000:])
     if verbose:
-        print(" ".join(cmd))
+        for c in [*cmds, link]:
+            print(" ".join(c))
     os.replace(tmp, LIB)
     return LIB
 

@@ -7,6 +7,7 @@
 #pragma once
 
 #include "kd_gemm.hpp"
+#include "kd_pad.hpp"
 #include <math.h>
 
 namespace kd {
@@ -808,21 +809,6 @@ __global__ __launch_bounds__(256) void transpose_bf16_vec_kernel(const uint16_t*
     *(u32x4*)(dst + (c0 + drow) * ld_dst + r0 + 8 * vr) = u32x4{w[0], w[1], w[2], w[3]};
   }
 }
-
-// dst[r][c] = src[r][c] for r < rows, c < cols; zero elsewhere in the
-// [dst_rows x ld_dst] destination.
-template <class E>
-__global__ __launch_bounds__(256) void pad_kernel(const typename E::T* src, int64_t ld_src, int64_t rows,
-                                                  int64_t cols, typename E::T* dst, int64_t ld_dst,
-                                                  int64_t dst_rows) {
-  typedef typename E::T T;
-  const int64_t n = dst_rows * ld_dst;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / ld_dst, c = i - r * ld_dst;
-    dst[i] = (r < rows && c < cols) ? src[r * ld_src + c] : (T)0;
-  }
-}
-
 
 // Online logsumexp across vocabulary strips, first level: for each chunk row
 // t and group of kMergeStrips strips, merge the per-strip (max, sum exp2)

@@ -26,6 +26,10 @@ constexpr int kHitT = 64;          // chunk rows of one forward-GEMM wave tile
 constexpr int kMergeStrips = 64;   // strips merged per first-level logsumexp group
 constexpr int kBlockRows = 32;     // cache builder: vocabulary rows per block maximum
 constexpr int kFbBatch = 1024;     // cache builder: ids per batch of the exact fallback
+constexpr int kActBlock = 128;     // 8-bit checkpoints: elements of a row that share a scale
+constexpr int kNormWaveMax = 6 * 512; // layer norm: widest row that one wave holds
+constexpr int kSampleTile = 1024;  // sampling: ids of one wave of the scan
+constexpr int kSampleGroup = 64;   // sampling: ids per stored maximum
 
 KD_HD constexpr int imin(int a, int b) { return a < b ? a : b; }
 KD_HD constexpr int imax(int a, int b) { return a > b ? a : b; }

@@ -81,8 +81,10 @@ struct Plan {
 
 // lean: one chunk per head-gradient launch (the smallest workspace; used by
 // the allocation-free entry point, whose workspace is a fixed static array).
+// act8: hidden comes as an 8-bit checkpoint and each chunk's rows are brought
+// back into the padded copy.
 inline int32_t make_plan(int64_t T, int64_t d, int64_t V, int64_t K, int64_t chunk, int32_t dt, int mode, Plan* p,
-                  bool lean = false) {
+                  bool lean = false, bool act8 = false) {
   if (dt != KD_BF16 && dt != KD_F32) return KD_ERR_DTYPE;
   if (T < 1 || d < 1 || V < 1 || K < 1 || K > V || K > KD_MAX_K) return KD_ERR_BAD_SHAPE;
   if (chunk < 1) return KD_ERR_BAD_CHUNK;
@@ -144,7 +146,7 @@ inline int32_t make_plan(int64_t T, int64_t d, int64_t V, int64_t K, int64_t chu
   P.off_scalar = o; o += 256;
   take(P.off_wt, B, (size_t)P.d_p * P.V_p * e);
   take(P.off_wp, P.pad_d, (size_t)V * P.d_p * e);
-  take(P.off_hp, P.pad_d, (size_t)P.R_p * P.d_p * e);
+  take(P.off_hp, P.pad_d || act8, (size_t)P.R_p * P.d_p * e);
   take(P.off_ht, B, (size_t)P.d_p * P.R_g * e);
   take(P.off_g, B, (size_t)P.R_p * P.V_p * e);
   take(P.off_gt, B, (size_t)P.V_p * P.R_g * e);
@@ -162,9 +164,10 @@ inline int32_t make_plan(int64_t T, int64_t d, int64_t V, int64_t K, int64_t chu
 }
 
 
-inline size_t workspace_for(int mode, int64_t T, int64_t d, int64_t V, int64_t K, int64_t chunk, int32_t in_dtype) {
+inline size_t workspace_for(int mode, int64_t T, int64_t d, int64_t V, int64_t K, int64_t chunk, int32_t in_dtype,
+                            bool act8 = false) {
   Plan p;
-  if (make_plan(T, d, V, K, chunk, in_dtype, mode, &p) != KD_OK) return 0;
+  if (make_plan(T, d, V, K, chunk, in_dtype, mode, &p, false, act8) != KD_OK) return 0;
   return p.total;
 }
 
@@ -225,6 +228,62 @@ inline int32_t make_cache_plan(int64_t T, int64_t d, int64_t V, int64_t K, int64
   P.off_ovf = o; o = align256(o + (size_t)P.R_p * sizeof(int));
   P.off_z = o; o = align256(o + (size_t)P.R_p * P.V_p * sizeof(float));                   // [R_p][V_p] logits
   P.total = o;
+  return KD_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Operators around the head (see kd_norm.hpp, kd_logits.hpp, kd_sample.hpp)
+// ---------------------------------------------------------------------------
+
+// Layer norm backward: blocks of rows, one partial weight-gradient row each.
+// Two blocks of four waves fit a CU (the accumulators take about 230
+// registers at d = 2880); fewer rows per wave than two would spend as much on
+// the partial rows as on the data.
+inline int64_t norm_bwd_blocks(int64_t T, int64_t d) {
+  const int64_t rows = d <= kNormWaveMax ? 4 : 1;          // rows in flight per block
+  return std::max<int64_t>(1, std::min<int64_t>(2 * kNumCU, cdiv(T, 2 * rows)));
+}
+inline size_t norm_bwd_workspace(int64_t T, int64_t d) {
+  return align256((size_t)norm_bwd_blocks(T, d) * 2 * (size_t)d * sizeof(float));
+}
+
+// Head logits: rows up to kSkinnyRows take the product that reads W once;
+// more run on the GEMM, kLogitRows at a time.
+constexpr int64_t kSkinnyRows = 32;
+constexpr int64_t kLogitRows = 8192;
+struct LogitsPlan {
+  bool skinny, pad_w, pad_h;
+  int64_t d_p, rows;
+  size_t off_wp, off_hp, total;
+};
+// aligned_w / aligned_h: every row of W / hidden starts at a multiple of 16
+// bytes (and hidden's stride is within the GEMM's 32-bit tile offsets).
+inline int32_t make_logits_plan(int64_t T, int64_t d, int64_t V, int32_t dt, bool aligned_w, bool aligned_h,
+                                LogitsPlan* p) {
+  if (dt != KD_BF16 && dt != KD_F32) return KD_ERR_DTYPE;
+  if (T < 1 || d < 1 || V < 1 || T > (1ll << 24) || d > (1ll << 20) || V > (1ll << 24)) return KD_ERR_BAD_SHAPE;
+  const int64_t eb = dt == KD_BF16 ? 2 : 4;
+  p->skinny = T <= kSkinnyRows;
+  p->d_p = round_up(d, 64);
+  p->rows = std::min<int64_t>(T, kLogitRows);
+  p->pad_w = !p->skinny && (d % 64 != 0 || !aligned_w);
+  p->pad_h = !p->skinny && (d % 64 != 0 || !aligned_h);
+  size_t o = 0;
+  p->off_wp = o;
+  if (p->pad_w) o = align256(o + (size_t)V * p->d_p * eb);
+  p->off_hp = o;
+  if (p->pad_h) o = align256(o + (size_t)p->rows * p->d_p * eb);
+  p->total = o;
+  return KD_OK;
+}
+
+// Sampling: one maximum per group and one mass per tile of every row.
+inline int32_t sample_plan(int64_t R, int64_t V, size_t* off_mass, size_t* total) {
+  if (R < 1 || V < 1 || V > (1ll << 24)) return KD_ERR_BAD_SHAPE;
+  // one launch covers all rows: its threads are counted in 32 bits
+  if (R > (1ll << 21) || R * cdiv(cdiv(V, kSampleTile), 4) >= (1ll << 24)) return KD_ERR_BAD_SHAPE;
+  *off_mass = align256((size_t)R * cdiv(V, kSampleGroup) * sizeof(float));
+  *total = align256(*off_mass + (size_t)R * cdiv(V, kSampleTile) * sizeof(double));
   return KD_OK;
 }
 

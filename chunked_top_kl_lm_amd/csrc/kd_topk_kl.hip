@@ -30,8 +30,11 @@
 
 #include <mutex>
 
+#include "../../include/kd_head_ops.h"
 #include "../../include/kd_topk_kl.h"
+#include "kd_act8.hpp"
 #include "kd_cache.hpp"
+#include "kd_launch.hpp"
 #include "kd_plan.hpp"
 #include "kd_kernels.hpp"
 #include "kd_probe.hpp"
@@ -41,32 +44,7 @@ namespace {
 
 // (tile configurations, the plan and the workspace carve-up: kd_plan.hpp)
 
-// One block per tile (a multiple of 8 blocks).
-template <class TC, class E, class Epi>
-hipError_t launch_gemm(const GemmShape& g, const Epi& epi, hipStream_t st) {
-  const int nb = g.tiles_m * g.tiles_n * g.splits;
-  const int grid = (nb + 7) & ~7;
-  hipLaunchKernelGGL((gemm_nt_kernel<E, TC::BM, TC::BN, TC::WM, TC::WN, TC::STAGES, Epi, TC::RB>), dim3(grid),
-                     dim3(TC::kThreads), 0, st, g, epi);
-  return hipGetLastError();
-}
-
-// group_m: row tiles per group of the tile order (see tile_position).  The
-// head-gradient GEMM uses 4 (it re-streams its 11.8 MB H_c^T operand once
-// per row band otherwise); the others measured best with 1.
-template <class TC>
-GemmShape make_shape(const void* A, int64_t lda, int M, const void* B, int64_t ldb, int N, int64_t k_bytes,
-                     int splits, int group_m) {
-  GemmShape g;
-  g.group_m = group_m;
-  g.A = A; g.B = B; g.lda = lda; g.ldb = ldb; g.M = M; g.N = N;
-  g.k_tiles = (int)(k_bytes / TC::RB);
-  g.k_tiles_per_split = (int)cdiv(g.k_tiles, splits);
-  g.splits = (int)cdiv(g.k_tiles, g.k_tiles_per_split);   // <= splits; no split is empty
-  g.tiles_m = (int)cdiv(M, TC::BM);
-  g.tiles_n = (int)cdiv(N, TC::BN);
-  return g;
-}
+// (GEMM launches: kd_launch.hpp)
 
 // dst [gy*64 x ld_dst] = transpose of src [rows x cols] (ld_src), zero
 // padded; 16-byte accesses when the layout allows it.
@@ -81,11 +59,6 @@ void launch_transpose(const typename E::T* src, int64_t ld_src, int64_t rows, in
   else
     hipLaunchKernelGGL(transpose_pad_kernel<E>, dim3(gx, gy), dim3(256), 0, st, src, ld_src, rows, cols, dst, ld_dst);
 }
-
-#define KD_LAUNCH_CHECK()                         \
-  do {                                            \
-    if (hipGetLastError() != hipSuccess) return KD_ERR_HIP; \
-  } while (0)
 
 // Pointers of one call (see the entry points for which a mode uses).
 struct Args {
@@ -107,6 +80,8 @@ struct Args {
   int32_t* status;
   hipStream_t st;
   void* const* events;     // fused timing markers or NULL
+  const int8_t* q;         // backward: hidden as an 8-bit checkpoint (hidden is NULL), or NULL
+  const float* q_scale;
 };
 
 template <class E>
@@ -183,8 +158,14 @@ int32_t run(const Plan& P, const Args& A, char* ws) {
     mark(slot + 0, 0);
     const T* Hc = (const T*)A.hidden + c0 * d;
     const T* Hsrc = Hc;
-    int64_t ldh = d;
-    if (P.pad_d) {
+    int64_t ldh = d, ldc = d;
+    if (A.q) {
+      // the chunk's rows from their 8-bit checkpoint, zero-padded
+      launch_act8_dequantize<T>(A.q + c0 * d, A.q_scale + c0 * cdiv(d, kActBlock), R, d, Hp, P.d_p, Rt, st);
+      KD_LAUNCH_CHECK();
+      Hc = Hsrc = Hp;
+      ldh = ldc = P.d_p;
+    } else if (P.pad_d) {
       const int64_t n = Rt * P.d_p;
       hipLaunchKernelGGL(pad_kernel<E>, dim3((unsigned)std::min<int64_t>(cdiv(n, 256), 65536)), dim3(256), 0, st,
                          Hc, d, (int64_t)R, d, Hp, P.d_p, Rt);
@@ -194,7 +175,7 @@ int32_t run(const Plan& P, const Args& A, char* ws) {
     }
     if (want_dw) {
       // H_c^T, zero-padded to [d_p][R_p], into the chunk's slot of the group
-      launch_transpose<E>(Hc, d, (int64_t)R, d, Ht + gslot * P.R_p, P.R_g, (unsigned)(P.R_p / 64),
+      launch_transpose<E>(Hc, ldc, (int64_t)R, d, Ht + gslot * P.R_p, P.R_g, (unsigned)(P.R_p / 64),
                           (unsigned)(P.d_p / 64), st);
       KD_LAUNCH_CHECK();
     }
@@ -342,7 +323,7 @@ int32_t dispatch(int mode, int32_t in_dtype, int64_t T, int64_t d, int64_t V, in
                  void* workspace, size_t workspace_bytes, const Args& A, bool lean = false) {
   if (!(A.tau > 0.f) || !isfinite(A.tau)) return KD_ERR_BAD_TAU;
   Plan p;
-  const int32_t st = make_plan(T, d, V, K, chunk, in_dtype, mode, &p, lean);
+  const int32_t st = make_plan(T, d, V, K, chunk, in_dtype, mode, &p, lean, A.q != nullptr);
   if (st != KD_OK) return st;
   if ((((uintptr_t)A.hidden) | ((uintptr_t)A.W)) & 15) return KD_ERR_BAD_SHAPE;
   if (lean && p.total > workspace_bytes) return KD_ERR_NOALLOC_SIZE;
@@ -573,19 +554,20 @@ int32_t kd_topk_kl_fwd_timed(const void* hidden, const void* W, int32_t in_dtype
                   row_kl, workspace, workspace_bytes, status_dev, stream, events);
 }
 
-static int32_t bwd_impl(const void* hidden, const void* W, int32_t in_dtype, const int32_t* teacher_idx,
+// hidden, or with hidden NULL its 8-bit checkpoint (q, q_scale)
+static int32_t bwd_impl(const void* hidden, const int8_t* q, const float* q_scale, const void* W, int32_t in_dtype, const int32_t* teacher_idx,
                         const float* teacher_logit, const uint8_t* mask, int64_t T, int64_t d, int64_t V, int64_t K,
                         float tau, int64_t chunk, const float* row_lse, const float* grad_loss, void* grad_hidden,
                         int32_t grad_hidden_dtype, float* grad_W, int32_t accumulate_grad_W, uint16_t* grad_W_bf16,
                         void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream,
                         void* const* events) {
-  if (!hidden || !W || !teacher_idx || !teacher_logit || !row_lse) return KD_ERR_NULL_ARG;
+  if ((!hidden && !q) || !W || !teacher_idx || !teacher_logit || !row_lse) return KD_ERR_NULL_ARG;
   if (!grad_hidden && !grad_W) return KD_ERR_NULL_ARG;
   if (grad_W_bf16 && !grad_W) return KD_ERR_NULL_ARG;
   if (grad_hidden_dtype != KD_F32 && grad_hidden_dtype != KD_BF16) return KD_ERR_DTYPE;
   kd::Args a{hidden, W, teacher_idx, teacher_logit, mask, tau, nullptr, const_cast<float*>(row_lse), nullptr,
              grad_loss, grad_hidden, grad_hidden_dtype, grad_W, accumulate_grad_W ? 1 : 0, grad_W_bf16, status_dev,
-             (hipStream_t)stream, events};
+             (hipStream_t)stream, events, q, q_scale};
   return kd::dispatch(kd::kBackward, in_dtype, T, d, V, K, chunk, workspace, workspace_bytes, a);
 }
 
@@ -594,7 +576,7 @@ int32_t kd_topk_kl_bwd(const void* hidden, const void* W, int32_t in_dtype, cons
                        float tau, int64_t chunk, const float* row_lse, const float* grad_loss, void* grad_hidden,
                        int32_t grad_hidden_dtype, float* grad_W, int32_t accumulate_grad_W, uint16_t* grad_W_bf16,
                        void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream) {
-  return bwd_impl(hidden, W, in_dtype, teacher_idx, teacher_logit, mask, T, d, V, K, tau, chunk, row_lse, grad_loss,
+  return bwd_impl(hidden, nullptr, nullptr, W, in_dtype, teacher_idx, teacher_logit, mask, T, d, V, K, tau, chunk, row_lse, grad_loss,
                   grad_hidden, grad_hidden_dtype, grad_W, accumulate_grad_W, grad_W_bf16, workspace,
                   workspace_bytes, status_dev, stream, nullptr);
 }
@@ -606,9 +588,26 @@ int32_t kd_topk_kl_bwd_timed(const void* hidden, const void* W, int32_t in_dtype
                              uint16_t* grad_W_bf16, void* workspace, size_t workspace_bytes, int32_t* status_dev,
                              void* stream, void* const* events) {
   if (!events) return KD_ERR_NULL_ARG;
-  return bwd_impl(hidden, W, in_dtype, teacher_idx, teacher_logit, mask, T, d, V, K, tau, chunk, row_lse, grad_loss,
+  return bwd_impl(hidden, nullptr, nullptr, W, in_dtype, teacher_idx, teacher_logit, mask, T, d, V, K, tau, chunk, row_lse, grad_loss,
                   grad_hidden, grad_hidden_dtype, grad_W, accumulate_grad_W, grad_W_bf16, workspace,
                   workspace_bytes, status_dev, stream, events);
+}
+
+size_t kd_topk_kl_bwd_act8_workspace_bytes(int64_t T, int64_t d, int64_t V, int64_t K, int64_t chunk,
+                                           int32_t in_dtype) {
+  return kd::workspace_for(kd::kBackward, T, d, V, K, chunk, in_dtype, true);
+}
+
+int32_t kd_topk_kl_bwd_act8(const int8_t* q, const float* scale, const void* W, int32_t in_dtype,
+                            const int32_t* teacher_idx, const float* teacher_logit, const uint8_t* mask, int64_t T,
+                            int64_t d, int64_t V, int64_t K, float tau, int64_t chunk, const float* row_lse,
+                            const float* grad_loss, void* grad_hidden, int32_t grad_hidden_dtype, float* grad_W,
+                            int32_t accumulate_grad_W, uint16_t* grad_W_bf16, void* workspace,
+                            size_t workspace_bytes, int32_t* status_dev, void* stream) {
+  if (!q || !scale) return KD_ERR_NULL_ARG;
+  return bwd_impl(nullptr, q, scale, W, in_dtype, teacher_idx, teacher_logit, mask, T, d, V, K, tau, chunk, row_lse,
+                  grad_loss, grad_hidden, grad_hidden_dtype, grad_W, accumulate_grad_W, grad_W_bf16, workspace,
+                  workspace_bytes, status_dev, stream, nullptr);
 }
 
 size_t kd_topk_cache_workspace_bytes(int64_t T, int64_t d, int64_t V, int64_t K, int64_t chunk, int32_t in_dtype) {
@@ -669,6 +668,7 @@ const char* kd_status_str(int32_t s) {
     case KD_ERR_NOALLOC_SIZE:
       return "the sizes need more workspace than the allocation-free entry point's fixed device scratch "
              "(KD_NOALLOC_SCRATCH_BYTES) holds";
+    case KD_ERR_BAD_PARAM: return "eps, temperature, top_k, top_p or min_p is outside its range";
     default: return "unknown status";
   }
 }
