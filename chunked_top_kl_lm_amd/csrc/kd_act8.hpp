@@ -25,36 +25,52 @@
 
 namespace kd {
 
-// Magnitude bits of the largest of eight values (a NaN's lie above Inf's).
+// Magnitude bits, doubled, of the largest of eight values (the shift drops
+// the sign; a NaN's lie above Inf's, Inf's above every finite value's).
 __device__ __forceinline__ uint32_t amax_bits(const Vec8& x) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x.v[i]) & 0x7fffffffu);
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x.v[i]) << 1);
   return m;
 }
 // Maximum over the 16 lanes that share a block, left in each of them.
 __device__ __forceinline__ uint32_t block_max16(uint32_t m) {
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
-  return m;
+  return lanes_reduce<16>(m, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
-// The block's scale from its largest magnitude bits.
+// The block's scale from its largest magnitude bits (doubled).
 __device__ __forceinline__ float act8_scale(uint32_t amax) {
-  if (amax >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-  return fmaxf(__uint_as_float(amax) * (1.0f / 127.0f), 1.17549435e-38f);
+  if (amax >= 0xff000000u) return __uint_as_float(0x7fc00000u);
+  return fmaxf(__uint_as_float(amax >> 1) * (1.0f / 127.0f), 1.17549435e-38f);
 }
 
 // Eight quantised elements as 8 bytes; inv = 1 / scale (NaN: all zero).
+// rint by adding 1.5 * 2^23: the sum's low byte is the integer in two's
+// complement.  |x * inv| <= 127 (1 + 4 * 2^-24), so the integer needs no
+// clamp.  v_perm gathers the bytes, three per four elements.
 __device__ __forceinline__ uint2 act8_pack(const Vec8& x, float inv) {
-  uint32_t w[2] = {0, 0};
+  uint32_t b[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float r = fminf(fmaxf(rintf(x.v[i] * inv), -127.f), 127.f);
-    const int q = inv == inv ? (int)r : 0;
-    w[i >> 2] |= ((uint32_t)q & 255u) << (8 * (i & 3));
+    float t = x.v[i] * inv;
+    asm("" : "+v"(t));                              // two roundings: no fma of product and sum
+    b[i] = __float_as_uint(t + 12582912.0f);
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x0c0c0400u);
+    w[h] = inv == inv ? lo | (hi << 16) : 0;
   }
   return make_uint2(w[0], w[1]);
+}
+
+// One element as a byte.
+__device__ __forceinline__ int8_t act8_one(float x, float inv) {
+  float t = x * inv;
+  asm("" : "+v"(t));
+  return inv == inv ? (int8_t)(__float_as_uint(t + 12582912.0f) & 255u) : (int8_t)0;
 }
 
 // Quantise the lane's eight elements (c a multiple of 8, the 16 lanes of a

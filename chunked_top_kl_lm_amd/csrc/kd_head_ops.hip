@@ -124,7 +124,7 @@ bool rows_aligned(const void* p, int64_t ld, int64_t eb) {
 // ---------------------------------------------------------------------------
 template <class E>
 int32_t sample_run(const SampleArgs& A, hipStream_t st) {
-  hipLaunchKernelGGL(sample_scan_kernel<E>, dim3((unsigned)(A.R * cdiv(A.tiles, 4))), dim3(256), 0, st, A);
+  hipLaunchKernelGGL(sample_scan_kernel<E>, dim3((unsigned)(A.R * A.segs)), dim3(kSampleScan), 0, st, A);
   KD_LAUNCH_CHECK();
   hipLaunchKernelGGL(sample_pick_kernel<E>, dim3((unsigned)A.R), dim3(kSamplePick), 0, st, A);
   KD_LAUNCH_CHECK();
@@ -249,8 +249,8 @@ int32_t kd_head_logits(const void* hidden, int64_t ldh, const void* W, int32_t i
 }
 
 size_t kd_sample_workspace_bytes(int64_t R, int64_t V) {
-  size_t off, total;
-  return kd::sample_plan(R, V, &off, &total) == KD_OK ? total : 0;
+  kd::SamplePlan p;
+  return kd::make_sample_plan(R, V, &p) == KD_OK ? p.total : 0;
 }
 
 int32_t kd_sample(const void* logits, int64_t ldz, int32_t dtype, int64_t R, int64_t V, const void* u,
@@ -260,8 +260,8 @@ int32_t kd_sample(const void* logits, int64_t ldz, int32_t dtype, int64_t R, int
                   void* stream) {
   if (!logits || !u || !token) return KD_ERR_NULL_ARG;
   if (!kd::known_dtype(dtype)) return KD_ERR_DTYPE;
-  size_t off, total;
-  const int32_t rc = kd::sample_plan(R, V, &off, &total);
+  kd::SamplePlan p;
+  const int32_t rc = kd::make_sample_plan(R, V, &p);
   if (rc != KD_OK) return rc;
   if (ldz < V) return KD_ERR_BAD_SHAPE;
   // (the comparisons refuse NaN)
@@ -272,7 +272,7 @@ int32_t kd_sample(const void* logits, int64_t ldz, int32_t dtype, int64_t R, int
       kd::misaligned(temperature_rows, 8) || kd::misaligned(top_k_rows, 4) || kd::misaligned(top_p_rows, 8) ||
       kd::misaligned(min_p_rows, 8) || kd::misaligned(token, 4) || kd::misaligned(logprob, 4))
     return KD_ERR_BAD_SHAPE;
-  if (!workspace || workspace_bytes < total || (((uintptr_t)workspace) & 255)) return KD_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < p.total || (((uintptr_t)workspace) & 255)) return KD_ERR_WORKSPACE;
   kd::SampleArgs A;
   A.z = logits; A.ldz = ldz; A.R = (int)R; A.V = (int)V;
   A.u = u; A.u_is_f64 = u_is_f64;
@@ -280,10 +280,13 @@ int32_t kd_sample(const void* logits, int64_t ldz, int32_t dtype, int64_t R, int
   A.top_k = (int)(top_k < V ? top_k : 0);
   A.temperature_rows = temperature_rows; A.top_k_rows = top_k_rows;
   A.top_p_rows = top_p_rows; A.min_p_rows = min_p_rows;
-  A.gmax = (float*)workspace;
-  A.tmass = (double*)((char*)workspace + off);
-  A.groups = (int)kd::cdiv(V, kd::kSampleGroup);
-  A.tiles = (int)kd::cdiv(V, kd::kSampleTile);
+  char* ws = (char*)workspace;
+  A.groups = (int)p.groups; A.segs = (int)p.segs;
+  A.gmax = (float*)(ws + p.off_gmax);
+  A.smax = (float*)(ws + p.off_smax);
+  A.smass = (double*)(ws + p.off_smass);
+  A.hlen = (int*)(ws + p.off_hlen);
+  A.hist = p.hist ? (uint64_t*)(ws + p.off_hist) : nullptr;
   A.token = token; A.logprob = logprob;
   hipStream_t st = (hipStream_t)stream;
   return dtype == KD_BF16 ? kd::sample_run<kd::Bf16>(A, st) : kd::sample_run<kd::F32>(A, st);

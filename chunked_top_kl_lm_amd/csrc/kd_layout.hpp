@@ -28,7 +28,9 @@ constexpr int kBlockRows = 32;     // cache builder: vocabulary rows per block m
 constexpr int kFbBatch = 1024;     // cache builder: ids per batch of the exact fallback
 constexpr int kActBlock = 128;     // 8-bit checkpoints: elements of a row that share a scale
 constexpr int kNormWaveMax = 6 * 512; // layer norm: widest row that one wave holds
-constexpr int kSampleTile = 1024;  // sampling: ids of one wave of the scan
+constexpr int kSampleSeg = 16384;  // sampling: ids of one block of the scan
+constexpr int kSampleBins = 2048;  // sampling: bins of T/64 below the largest logit; the last holds the rest
+constexpr int kSampleList = 4096;  // sampling: longest candidate list
 constexpr int kSampleGroup = 64;   // sampling: ids per stored maximum
 
 KD_HD constexpr int imin(int a, int b) { return a < b ? a : b; }

@@ -20,6 +20,8 @@
 // fixed order, so the results are the same bits from call to call.
 #pragma once
 
+#include <type_traits>
+
 #include "kd_act8.hpp"
 
 namespace kd {
@@ -50,6 +52,51 @@ template <int WPR> struct NormCfg {
   static constexpr int kRows = WPR == 1 ? 4 : 1;
   static constexpr int kThreads = 64 * WPR * kRows;
 };
+// Vectors of a row that every lane holds in each variant (a variant serves
+// rows wider than the next narrower one's); of the others a lane may have none.
+constexpr int norm_whole(int NV) { return NV == 6 ? 4 : NV / 2; }
+
+// The row's columns: lane vectors of eight up to d8 = d rounded down to a
+// multiple of 8, then up to seven single columns that lanes 0 .. tail - 1 of
+// one wave hold one each (the wave whose vectors go on there, so that it also
+// holds the rest of the last block of an 8-bit checkpoint).  No vector
+// crosses the row's end, and the code has one path.
+template <int WPR, int NV>
+struct NormCols {
+  static constexpr int S = 512 * WPR;              // columns per vector of every lane
+  int d, d8, tail, c0, lane;
+  bool owner;                                      // (uniform per wave) has the tail
+  __device__ __forceinline__ explicit NormCols(int d_) : d(d_), d8(d_ & ~7), tail(d_ & 7) {
+    lane = threadIdx.x & 63;
+    const int wave = WPR == 1 ? 0 : (int)(threadIdx.x >> 6);
+    c0 = 8 * (64 * wave + lane);
+    owner = tail > 0 && (d8 / 512) % WPR == wave;
+  }
+  __device__ __forceinline__ int col(int i) const { return c0 + i * S; }
+  __device__ __forceinline__ bool has(int i) const { return i < norm_whole(NV) || col(i) < d8; }
+  __device__ __forceinline__ bool has_tail() const { return owner && lane < tail; }
+  __device__ __forceinline__ int tail_vec() const { return d8 / S; }          // i of the slot after the last vector
+  __device__ __forceinline__ int tail_lane() const { return (d8 / 8) & 63; }  // its lane
+  // vector i of a row (zeros where the lane has none), its tail column
+  template <class T>
+  __device__ __forceinline__ Raw8<T> load(const T* row, int i) const {
+    Raw8<T> r = {};
+    if (has(i)) r = raw_load8(row + col(i));
+    return r;
+  }
+  template <class T>
+  __device__ __forceinline__ float load_tail(const T* row) const {
+    return has_tail() ? widen(row[d8 + lane]) : 0.f;
+  }
+  template <class T>
+  __device__ __forceinline__ void store(T* row, int i, const Vec8& v) const {
+    if (has(i)) store8(row + col(i), v);
+  }
+  template <class T>
+  __device__ __forceinline__ void store_tail(T* row, float v) const {
+    if (has_tail()) narrow(row + d8 + lane, v);
+  }
+};
 
 struct NormFwdArgs {
   const void* x;
@@ -69,55 +116,79 @@ struct NormFwdArgs {
 template <class T, class WT, int WPR, int NV, bool CKPT>
 __global__ __launch_bounds__(NormCfg<WPR>::kThreads) void norm_fwd_kernel(NormFwdArgs A) {
   __shared__ float2 s_red[2][WPR];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   constexpr int R = NormCfg<WPR>::kRows;
-  const int d = A.d, c0 = 8 * ((WPR == 1 ? 0 : 64 * wave) + lane);
+  const NormCols<WPR, NV> C(A.d);
+  const int wave = threadIdx.x >> 6, d = A.d;
   // one row per wave (or block) and launch; the loop only serves row counts
   // past the grid's limit
   for (int64_t t = (int64_t)blockIdx.x * R + (R > 1 ? wave : 0); t < A.T; t += (int64_t)gridDim.x * R) {
-  const T* xr = (const T*)A.x + t * A.ldx;
-  Vec8 x[NV];
+    const T* xr = (const T*)A.x + t * A.ldx;
+    Raw8<T> x[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) x[i] = row_load8(xr, c0 + i * 512 * WPR, d);
-  float s = 0.f;
+    for (int i = 0; i < NV; ++i) x[i] = C.load(xr, i);
+    const float xt = C.load_tail(xr);
+    float s = xt;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < NV; ++i) {
+      const Vec8 v = unpack(x[i]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += x[i].v[e];
-  }
-  const float mean = row_sum2<WPR>(s, 0.f, s_red[0]).x / (float)d;
-  float m2 = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float c = c0 + i * 512 * WPR + e < d ? x[i].v[e] - mean : 0.f;
-      m2 = fmaf(c, c, m2);
+      for (int e = 0; e < 8; ++e) s += v.v[e];
     }
-  }
-  const float rstd = 1.f / sqrtf(row_sum2<WPR>(m2, 0.f, s_red[1]).x / (float)d + A.eps);
-  T* yr = (T*)A.y + t * (int64_t)d;
+    const float mean = row_sum2<WPR>(s, 0.f, s_red[0]).x / (float)d;
+    float m2 = C.has_tail() ? (xt - mean) * (xt - mean) : 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = c0 + i * 512 * WPR;
-    if (i * 512 * WPR >= d) break;                 // uniform: no lane has a column here
-    if constexpr (CKPT) act8_store(x[i], A.q + t * (int64_t)d, A.scale + t * A.nb, c, d);
-    const Vec8 w = row_load8((const WT*)A.w, c, d);
-    Vec8 y;
-    if (A.b) {
-      const Vec8 b = row_load8((const WT*)A.b, c, d);
+    for (int i = 0; i < NV; ++i) {
+      keep(x[i]);
+      const Vec8 v = unpack(x[i]);
+      float q = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y.v[e] = fmaf((x[i].v[e] - mean) * rstd, w.v[e], b.v[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y.v[e] = (x[i].v[e] - mean) * rstd * w.v[e];
+      for (int e = 0; e < 8; ++e) q = fmaf(v.v[e] - mean, v.v[e] - mean, q);
+      m2 += C.has(i) ? q : 0.f;
     }
-    row_store8(yr, c, d, y);
-  }
-  if (lane == 0 && (WPR == 1 || wave == 0)) {
-    A.mean[t] = mean;
-    A.rstd[t] = rstd;
-  }
+    const float rstd = 1.f / sqrtf(row_sum2<WPR>(m2, 0.f, s_red[1]).x / (float)d + A.eps);
+    T* yr = (T*)A.y + t * (int64_t)d;
+    int8_t* qr = CKPT ? A.q + t * (int64_t)d : nullptr;
+    float* sr = CKPT ? A.scale + t * A.nb : nullptr;
+    uint32_t tail_bits = 0;
+    if (CKPT && C.owner)
+      tail_bits = read_lane(
+          lanes_reduce<8>(__float_as_uint(xt) << 1, [](uint32_t a, uint32_t b) { return max(a, b); }), 0);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i >= norm_whole(NV) && i * C.S >= d) break;   // uniform: no lane has a column here
+      keep(x[i]);
+      const Vec8 v = unpack(x[i]);
+      if constexpr (CKPT) {
+        uint32_t m = block_max16(amax_bits(v));
+        if (C.owner && i == C.tail_vec() && (C.tail_lane() ^ C.lane) < 16) m = max(m, tail_bits);
+        const float sc = act8_scale(m), inv = 1.f / sc;
+        const uint2 w = act8_pack(v, inv);
+        const int c = C.col(i);
+        if (C.has(i)) __builtin_memcpy(qr + c, &w, 8);
+        if ((c & (kActBlock - 1)) == 0 && c < d) sr[c / kActBlock] = sc;
+        if (C.owner && i == C.tail_vec()) {
+          const float inv_t = read_lane(inv, C.tail_lane());
+          if (C.has_tail()) qr[C.d8 + C.lane] = act8_one(xt, inv_t);
+        }
+      }
+      const Vec8 w = unpack(C.load((const WT*)A.w, i));
+      Vec8 y;
+      if (A.b) {
+        const Vec8 b = unpack(C.load((const WT*)A.b, i));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y.v[e] = fmaf((v.v[e] - mean) * rstd, w.v[e], b.v[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y.v[e] = (v.v[e] - mean) * rstd * w.v[e];
+      }
+      C.store(yr, i, y);
+    }
+    if (C.owner)
+      C.store_tail(yr, fmaf((xt - mean) * rstd, C.load_tail((const WT*)A.w), A.b ? C.load_tail((const WT*)A.b) : 0.f));
+    if (C.lane == 0 && (WPR == 1 || wave == 0)) {
+      A.mean[t] = mean;
+      A.rstd[t] = rstd;
+    }
   }
 }
 
@@ -135,52 +206,85 @@ struct NormBwdArgs {
   float* part;         // [blocks][2][d] partial dw and db, or NULL
 };
 
+// Rows of sixteen waves and four vectors (wider than 16384) are not held in
+// registers beside the accumulators: their second pass reads them again from
+// the L2.
+template <int WPR, int NV> constexpr bool norm_hold() { return WPR * NV < 64; }
+
 // Blocks of rows in turn: block b takes rows b, b + grid, ... (times kRows).
 template <class T, class WT, int WPR, int NV, bool CKPT>
 __global__ __launch_bounds__(NormCfg<WPR>::kThreads) void norm_bwd_kernel(NormBwdArgs A) {
+  typedef typename std::conditional<CKPT, int8_t, T>::type XT;
+  constexpr bool HOLD = norm_hold<WPR, NV>();
   __shared__ float2 s_red[2][WPR];
-  __shared__ float s_acc[WPR == 1 ? 2 * NV * 512 : 1];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int d = A.d, c0 = 8 * ((WPR == 1 ? 0 : 64 * wave) + lane);
+  __shared__ float s_acc[WPR == 1 ? 2 * NV * 512 + 16 : 1];
   constexpr int R = NormCfg<WPR>::kRows;
+  const NormCols<WPR, NV> C(A.d);
+  const int wave = threadIdx.x >> 6, lane = C.lane, d = A.d;
   Vec8 aw[NV], ab[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) aw[i].v[e] = ab[i].v[e] = 0.f;
+  float awt = 0.f, abt = 0.f;
   int flip = 0;
   const float inv_d = 1.f / (float)d;
+  const int64_t ldx = CKPT ? (int64_t)d : A.ldx;
+  const XT* xb = CKPT ? (const XT*)A.q : (const XT*)A.x;
   for (int64_t t = (int64_t)blockIdx.x * R + (R > 1 ? wave : 0); t < A.T; t += (int64_t)gridDim.x * R) {
     const float mean = A.mean[t], rstd = A.rstd[t];
-    Vec8 x[NV], dy[NV];
+    Raw8<XT> x[NV];
+    Raw8<T> dy[NV];
+    float sc[NV];
     const T* dyr = (const T*)A.dy + t * (int64_t)d;
+    const XT* xr = xb + t * ldx;
+    const float* sr = CKPT ? A.scale + t * A.nb : nullptr;
+    auto load = [&](int i) {
+      dy[i] = C.load(dyr, i);
+      x[i] = C.load(xr, i);
+      sc[i] = 1.f;
+      if constexpr (CKPT) sc[i] = C.has(i) ? sr[C.col(i) / kActBlock] : 0.f;
+    };
+    if constexpr (HOLD) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = c0 + i * 512 * WPR;
-      dy[i] = row_load8(dyr, c, d);
-      if constexpr (CKPT) x[i] = row_load8(A.q + t * (int64_t)d, c, d);
-      else x[i] = row_load8((const T*)A.x + t * A.ldx, c, d);
+      for (int i = 0; i < NV; ++i) load(i);
     }
-    float sg = 0.f, sgx = 0.f;
+    float xt = 0.f, gt = 0.f, wt = 0.f;
+    if (C.owner) {
+      gt = C.load_tail(dyr);
+      wt = C.load_tail((const WT*)A.w);
+      xt = C.load_tail(xr);
+      if constexpr (CKPT) xt *= sr[C.d8 / kActBlock];
+      xt = (xt - mean) * rstd;
+    }
+    // where a lane has no column, dy and w are zero, so every term below is too
+    auto xhat = [&](int i) {
+      Vec8 v = unpack(x[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v.v[e] = ((CKPT ? v.v[e] * sc[i] : v.v[e]) - mean) * rstd;
+      return v;
+    };
+    awt = fmaf(gt, xt, awt);
+    abt += gt;
+    float sg = gt * wt, sgx = gt * wt * xt;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = c0 + i * 512 * WPR;
-      float sc = 1.f;
-      if constexpr (CKPT) sc = c < d ? A.scale[t * A.nb + c / kActBlock] : 0.f;
-      const Vec8 w = row_load8((const WT*)A.w, c, d);
+      if constexpr (!HOLD) load(i);
+      const Vec8 w = unpack(C.load((const WT*)A.w, i));
+      const Vec8 g = unpack(dy[i]), xh = xhat(i);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        // columns past d: dy and w are zero there, so every term below is too
-        const float xe = CKPT ? x[i].v[e] * sc : x[i].v[e];
-        const float xh = c + e < d ? (xe - mean) * rstd : 0.f;
-        x[i].v[e] = xh;
-        aw[i].v[e] = fmaf(dy[i].v[e], xh, aw[i].v[e]);
-        ab[i].v[e] += dy[i].v[e];
-        const float g = dy[i].v[e] * w.v[e];
-        dy[i].v[e] = g;
-        sg += g;
-        sgx = fmaf(g, xh, sgx);
+        aw[i].v[e] = fmaf(g.v[e], xh.v[e], aw[i].v[e]);
+        ab[i].v[e] += g.v[e];
+        const float gw = g.v[e] * w.v[e];
+        sg += gw;
+        sgx = fmaf(gw, xh.v[e], sgx);
       }
+      // one vector at a time: the accumulators and the held row leave few
+      // registers
+      settle(aw[i]);
+      settle(ab[i]);
+      settle(sg, sgx);
     }
     const float2 m = row_sum2<WPR>(sg, sgx, s_red[flip]);
     flip ^= 1;
@@ -189,17 +293,28 @@ __global__ __launch_bounds__(NormCfg<WPR>::kThreads) void norm_bwd_kernel(NormBw
       T* dxr = (T*)A.dx + t * (int64_t)d;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        Vec8 o;
+        if (i >= norm_whole(NV) && i * C.S >= d) break;
+        if constexpr (HOLD) {
+          keep(dy[i]);
+          keep(x[i]);
+        } else {
+          load(i);
+        }
+        const Vec8 w = unpack(C.load((const WT*)A.w, i));
+        const Vec8 g = unpack(dy[i]);
+        Vec8 o = xhat(i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = rstd * (dy[i].v[e] - mg - x[i].v[e] * mgx);
-        row_store8(dxr, c0 + i * 512 * WPR, d, o);
+        for (int e = 0; e < 8; ++e) o.v[e] = rstd * (fmaf(g.v[e], w.v[e], -mg) - o.v[e] * mgx);
+        C.store(dxr, i, o);
       }
+      if (C.owner) C.store_tail(dxr, rstd * (fmaf(gt, wt, -mg) - xt * mgx));
     }
   }
   if (!A.part) return;
   float* pw = A.part + (int64_t)blockIdx.x * 2 * d;
   if constexpr (WPR == 1) {
     // join the four waves' columns, in the order of the waves
+    float* s_tail = s_acc + 2 * NV * 512;
     for (int w = 0; w < 4; ++w) {
       if (wave == w) {
 #pragma unroll
@@ -211,6 +326,10 @@ __global__ __launch_bounds__(NormCfg<WPR>::kThreads) void norm_bwd_kernel(NormBw
             s_acc[at] = w ? s_acc[at] + aw[i].v[e] : aw[i].v[e];
             s_acc[NV * 512 + at] = w ? s_acc[NV * 512 + at] + ab[i].v[e] : ab[i].v[e];
           }
+        if (C.has_tail()) {
+          s_tail[lane] = w ? s_tail[lane] + awt : awt;
+          s_tail[8 + lane] = w ? s_tail[8 + lane] + abt : abt;
+        }
       }
       __syncthreads();
     }
@@ -218,14 +337,21 @@ __global__ __launch_bounds__(NormCfg<WPR>::kThreads) void norm_bwd_kernel(NormBw
       Vec8 o;
 #pragma unroll
       for (int e = 0; e < 8; ++e) o.v[e] = s_acc[(i * 8 + e) * 64 + lane];
-      row_store8(pw + (i < NV ? 0 : d), 512 * (i < NV ? i : i - NV) + 8 * lane, d, o);
+      const int c = 512 * (i < NV ? i : i - NV) + 8 * lane;
+      if (c < C.d8) store8(pw + (i < NV ? 0 : d) + c, o);
+    }
+    if (wave == 0 && C.has_tail()) {
+      pw[C.d8 + lane] = s_tail[lane];
+      pw[d + C.d8 + lane] = s_tail[8 + lane];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      row_store8(pw, c0 + i * 512 * WPR, d, aw[i]);
-      row_store8(pw + d, c0 + i * 512 * WPR, d, ab[i]);
+      C.store(pw, i, aw[i]);
+      C.store(pw + d, i, ab[i]);
     }
+    C.store_tail(pw, awt);
+    C.store_tail(pw + d, abt);
   }
 }
 
@@ -236,8 +362,11 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, in
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int j = blockIdx.x * 64 + lane;
   float a = 0.f;
-  if (j < 2 * d)
-    for (int b = wave; b < blocks; b += 16) a += part[(int64_t)b * 2 * d + j];
+  if (j < 2 * d) {
+    const float* p = part + j;
+#pragma unroll 8
+    for (int b = wave; b < blocks; b += 16) a += p[(int64_t)b * 2 * d];
+  }
   s[wave][lane] = a;
   __syncthreads();
   if (wave == 0 && j < 2 * d) {

@@ -277,13 +277,32 @@ inline int32_t make_logits_plan(int64_t T, int64_t d, int64_t V, int32_t dt, boo
   return KD_OK;
 }
 
-// Sampling: one maximum per group and one mass per tile of every row.
-inline int32_t sample_plan(int64_t R, int64_t V, size_t* off_mass, size_t* total) {
+// Sampling: a maximum per group and, per segment of every row, its maximum,
+// mass and histogram (none where the candidate list holds the vocabulary).
+struct SamplePlan {
+  int64_t groups, segs;
+  bool hist;
+  size_t off_gmax, off_smax, off_smass, off_hlen, off_hist, total;
+};
+inline int32_t make_sample_plan(int64_t R, int64_t V, SamplePlan* p) {
   if (R < 1 || V < 1 || V > (1ll << 24)) return KD_ERR_BAD_SHAPE;
+  p->groups = cdiv(V, kSampleGroup);
+  p->segs = cdiv(V, kSampleSeg);
+  p->hist = V > kSampleList;
   // one launch covers all rows: its threads are counted in 32 bits
-  if (R > (1ll << 21) || R * cdiv(cdiv(V, kSampleTile), 4) >= (1ll << 24)) return KD_ERR_BAD_SHAPE;
-  *off_mass = align256((size_t)R * cdiv(V, kSampleGroup) * sizeof(float));
-  *total = align256(*off_mass + (size_t)R * cdiv(V, kSampleTile) * sizeof(double));
+  if (R > (1ll << 21) || R * p->segs > (1ll << 22)) return KD_ERR_BAD_SHAPE;
+  const size_t n = (size_t)(R * p->segs);
+  size_t o = 0;
+  auto take = [&](size_t& off, size_t bytes) {
+    off = o;
+    o = align256(o + bytes);
+  };
+  take(p->off_gmax, (size_t)R * p->groups * sizeof(float));
+  take(p->off_smax, n * sizeof(float));
+  take(p->off_smass, n * sizeof(double));
+  take(p->off_hlen, n * sizeof(int32_t));
+  take(p->off_hist, p->hist ? n * kSampleBins * sizeof(uint64_t) : 0);
+  p->total = o;
   return KD_OK;
 }
 

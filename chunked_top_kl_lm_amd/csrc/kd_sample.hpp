@@ -7,24 +7,33 @@
 // the ids with w_v >= min_p.  The drawn id is the first, in id order, whose
 // inclusive mass exceeds u times the kept mass.
 //
-// Borders between ids are decided in 64 bits.  w is a double (a polynomial of
-// degree 12, relative error about 1e-14 with its argument's rounding), and
-// masses are sums of 64-bit integers, W_v = rint(w_v 2^s) with s = 62 -
-// ceil(log2 V) (at most 52): integer sums are exact and do not depend on
-// their order, so LDS atomics keep the result the same from call to call.
-// An id more than 32 T below the largest logit (w < 1.3e-14) has W = 0.
-// NaN and -inf logits have no mass; a +inf logit is the largest and shares
-// the mass with its equals only.
+// Borders between ids are decided in 64 bits: w is a double from a polynomial
+// (relative error about 1e-14), and masses that ids are picked by are sums of
+// 64-bit integers, W_v = rint(w_v 2^s) with s = 62 - ceil(log2 V), at most 52:
+// integer sums do not depend on their order, so LDS atomics keep the result
+// the same from call to call.  An id more than about 32 T below the largest
+// logit (w < 1.3e-14) has W = 0.  NaN and -inf logits have no mass; a +inf
+// logit is the largest and shares the mass with its equals only.
 //
-// Bound by HBM: R V e bytes read once.  sample_scan_kernel makes that one
-// pass with all of the chip: per 64 ids the largest logit and, where the mass
-// of a whole row is needed, per 1024 ids the mass relative to the tile's own
-// largest logit.  sample_pick_kernel (one block per row) then reads back
-// only the 64-id groups that can hold kept ids: ids are put in 2047 bins of
-// T/64 below m, and the groups' maxima say how deep the list must go.  Rows
-// whose kept set is too long for a list (a flat row under top_p) are
-// streamed again: a histogram of mass over the bins, the one bin at the
-// border sorted, then the tiles' kept masses.
+// Bound by HBM: R V e bytes, read once by sample_scan_kernel with all of the
+// chip (a block per row and 16384 ids): the largest logit of every 64 ids,
+// and what the row's filters need: nothing (top_k), the segment's mass (no
+// filter), or a histogram of its mass over bins of T/64 (top_p, min_p).  The
+// bins lie on a grid of absolute logits, so that no block has to know the
+// row's largest logit; a bin's mass is kept relative to its upper edge, where
+// exp needs six terms only.
+//
+// sample_pick_kernel (a block per row) then
+//  - finds from the group maxima (top_k) or from the joined histogram how far
+//    below the largest logit kept ids can lie;
+//  - when few ids lie that high, reads back only their 64-id groups and ranks
+//    them (up to 256 by counting, more by sorting);
+//  - otherwise (a flat row) reads the row once more for the ids of the border
+//    bin alone: the bins above it are kept whole, and the segments' kept
+//    masses come from their histograms, so only one segment is looked into.
+// Rows that neither suits (more than 4096 equal logits at the border, top_k
+// past the list, temperatures that put the grid beyond 2^22 bins) stream the
+// row several times.
 #pragma once
 
 #include "kd_layout.hpp"
@@ -33,10 +42,11 @@
 
 namespace kd {
 
-constexpr int kSampleBins = 2048;     // bins of T/64 below the largest logit; the last holds the rest
-constexpr int kSampleList = 4096;     // longest candidate list (LDS)
 constexpr int kSamplePick = 1024;     // threads per row
-constexpr int kSampleTopGroups = 512; // top_p alone: groups whose maxima bound the first list
+constexpr int kSampleScan = 512;      // threads per segment
+constexpr int kSampleRank = 256;      // longest list that is ranked by counting
+constexpr int kSampleSub = 256;       // parts of the border's bins
+constexpr float kSampleGrid = 4194304.f;   // largest |logit| in bins that the grid takes
 
 struct SampleArgs {
   const void* z;
@@ -50,9 +60,12 @@ struct SampleArgs {
   const int32_t* top_k_rows;
   const double* top_p_rows;
   const double* min_p_rows;
-  float* gmax;                        // [R][groups]
-  double* tmass;                      // [R][tiles]
-  int groups, tiles;
+  int groups, segs;
+  float* gmax;                        // [R][groups] largest logit of a group
+  float* smax;                        // [R][segs] of a segment
+  double* smass;                      // [R][segs] its mass relative to smax
+  int* hlen;                          // [R][segs] bins of its histogram
+  uint64_t* hist;                     // [R][segs][kSampleBins], bin 0 that of smax; NULL: V fits the list
   int32_t* token;
   float* logprob;                     // or NULL
 };
@@ -62,8 +75,8 @@ struct SampleArgs {
 // setting (temperature <= 0 or NaN: the largest logit; top_p <= 0: the first
 // id; min_p > 1: w = 1 only).
 struct SampleRow {
-  double c;          // log2(e) / T
-  float cb;          // 64 / T
+  double c64;        // 64 / T: logits in bins
+  float cb;          // the same, rounded: what bins are formed with
   double top_p, min_p;
   int top_k;         // 0: off
   bool greedy;
@@ -78,22 +91,25 @@ __device__ __forceinline__ SampleRow sample_row(const SampleArgs& A, int r) {
   p.top_p = tp < 1.0 ? tp : 1.0;
   p.min_p = mp > 0.0 ? (mp < 1.0 ? mp : 1.0) : 0.0;
   p.greedy = !(t > 0.0) || p.top_k == 1 || p.top_p <= 0.0;
-  p.c = 1.4426950408889634 / t;
-  p.cb = (float)(64.0 / t);
+  p.c64 = 64.0 / t;
+  p.cb = (float)p.c64;
   return p;
 }
-// The mass of the whole row is needed: no top_k, and not min_p alone.
-__device__ __forceinline__ bool sample_needs_mass(const SampleRow& p) {
-  return !p.greedy && p.top_k == 0 && (p.top_p < 1.0 || p.min_p == 0.0);
+// What the scan leaves per segment of a row.
+enum SampleScanMode { kScanMax = 0, kScanMass = 1, kScanHist = 2 };
+__device__ __forceinline__ int sample_scan_mode(const SampleArgs& A, const SampleRow& p) {
+  if (p.greedy || p.top_k > 0) return kScanMax;
+  if (p.top_p == 1.0 && p.min_p == 0.0) return kScanMass;
+  return kScanHist;
 }
 
 // A logit as the operator sees it: NaN as -inf, -0 as +0.
 __device__ __forceinline__ float sample_logit(float x) { return x == x ? x + 0.f : -INFINITY; }
 
-// w = 2^((l - m) c).  2^f on |f| <= 1/2 by its Taylor series in f ln 2 up to
-// degree 12 (remainder 0.3466^13 / 13! < 2e-16).
-__device__ __forceinline__ double sample_weight(float l, float m, double c) {
-  const double y0 = ((double)l - (double)m) * c;
+// exp((l - m) c64 / 64).  2^f on |f| <= 1/2 by the Taylor series of exp in
+// f ln 2 up to degree 12 (remainder 0.3466^13 / 13! < 2e-16).
+__device__ __forceinline__ double sample_weight(float l, float m, double c64) {
+  const double y0 = ((double)l - (double)m) * (c64 * (1.4426950408889634 / 64.0));
   const double y = y0 > -64.0 ? y0 : -64.0;        // also NaN (inf - inf, inf * 0)
   const double k = rint(y);
   const double f = (y - k) * 0.6931471805599453;
@@ -114,18 +130,30 @@ __device__ __forceinline__ double sample_weight(float l, float m, double c) {
   const double w = __longlong_as_double(__double_as_longlong(p) + (long long)(int)k * (1ll << 52));
   return l == m ? 1.0 : (y0 > -64.0 ? w : 0.0);
 }
-// Bin of a logit: non-increasing in l.  The last bin has no mass.
-__device__ __forceinline__ int sample_bin(float l, float m, float cb) {
-  const float x = fminf((m - l) * cb, (float)(kSampleBins - 1));   // NaN (inf * 0): the last bin
-  return l == m ? 0 : (l == -INFINITY ? kSampleBins - 1 : (int)x);
+// exp(y / 64) for |y| <= 1.5 (a logit against its bin's edge): degree 6,
+// remainder 0.0235^7 / 7! < 1e-15.
+__device__ __forceinline__ double edge_weight(double y) {
+  const double x = y * (1.0 / 64.0);
+  double p = 1.0 / 720.0;
+  p = fma(p, x, 1.0 / 120.0);
+  p = fma(p, x, 1.0 / 24.0);
+  p = fma(p, x, 1.0 / 6.0);
+  p = fma(p, x, 0.5);
+  p = fma(p, x, 1.0);
+  return fma(p, x, 1.0);
+}
+// Units of the masses, 2^s.
+__device__ __forceinline__ double sample_scale(int V) {
+  const int bits = 62 - (32 - __clz(max(V - 1, 1)));
+  return (double)(1ull << min(bits, 52));
 }
 
-// Eight or four consecutive logits of a row (-inf past its end).
+// 16 bytes of consecutive logits of a row (-inf past its end).
 template <class E> struct SampleVec;
 template <> struct SampleVec<Bf16> { static constexpr int N = 8; };
 template <> struct SampleVec<F32> { static constexpr int N = 4; };
 template <class E>
-__device__ __forceinline__ void sample_load(const typename E::T* row, int v, int V, float (&x)[SampleVec<E>::N]) {
+__device__ __forceinline__ void sample_load(const typename E::T* row, int v, int V, float* x) {
   constexpr int N = SampleVec<E>::N;
   if (v + N <= V) {
     u32x4 u;
@@ -143,65 +171,85 @@ __device__ __forceinline__ void sample_load(const typename E::T* row, int v, int
   for (int i = 0; i < N; ++i) x[i] = sample_logit(x[i]);
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
-}
-template <class T>
-__device__ __forceinline__ T wave_add(T v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-template <class T>
-__device__ __forceinline__ T wave_incl_scan(T v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const T u = __shfl_up(v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-
-// Grid: for each row, its groups of 4 tiles.
+// A block per row and segment; 32 ids per thread, held in registers.
 template <class E>
-__global__ __launch_bounds__(256) void sample_scan_kernel(SampleArgs A) {
-  constexpr int N = SampleVec<E>::N, L = 16 / N;   // vectors per lane
-  constexpr int LG = kSampleGroup / N;             // lanes that share a group
-  const int quads = (A.tiles + 3) / 4;
-  const int r = blockIdx.x / quads, lane = threadIdx.x & 63;
-  const int tile = (blockIdx.x - r * quads) * 4 + (threadIdx.x >> 6);
-  if (tile >= A.tiles) return;
+__global__ __launch_bounds__(kSampleScan) void sample_scan_kernel(SampleArgs A) {
+  constexpr int N = SampleVec<E>::N, L = kSampleSeg / (N * kSampleScan);
+  __shared__ float s_max[kSampleScan / 64];
+  __shared__ double s_sum[kSampleScan / 64];
+  __shared__ int s_len;
+  __shared__ unsigned long long s_hist[kSampleBins];
+  const int r = blockIdx.x / A.segs, seg = blockIdx.x - r * A.segs;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const typename E::T* row = (const typename E::T*)A.z + (int64_t)r * A.ldz;
   float x[L][N];
 #pragma unroll
-  for (int j = 0; j < L; ++j) sample_load<E>(row, tile * kSampleTile + j * 64 * N + lane * N, A.V, x[j]);
+  for (int j = 0; j < L; ++j) sample_load<E>(row, seg * kSampleSeg + (j * kSampleScan + tid) * N, A.V, x[j]);
   const SampleRow p = sample_row(A, r);
-  float tm = -INFINITY;
+  const int mode = sample_scan_mode(A, p);
+  float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < L; ++j) {
     float g = x[j][0];
 #pragma unroll
     for (int i = 1; i < N; ++i) g = fmaxf(g, x[j][i]);
-#pragma unroll
-    for (int o = 1; o < LG; o <<= 1) g = fmaxf(g, __shfl_xor(g, o));
-    const int gi = tile * (kSampleTile / kSampleGroup) + j * (64 / LG) + lane / LG;
-    if (lane % LG == 0 && gi < A.groups) A.gmax[(int64_t)r * A.groups + gi] = g;
-    tm = fmaxf(tm, g);
+    g = lanes_reduce<kSampleGroup / N>(g, [](float a, float b) { return fmaxf(a, b); });
+    const int gi = seg * (kSampleSeg / kSampleGroup) + (j * kSampleScan + tid) * N / kSampleGroup;
+    if (lane % (kSampleGroup / N) == 0 && gi < A.groups) A.gmax[(int64_t)r * A.groups + gi] = g;
+    m = fmaxf(m, g);
   }
-  if (!sample_needs_mass(p)) return;
-  tm = wave_max(tm);
-  double s = 0.0;
-  if (tm > -INFINITY) {
+  m = wave_max(m);
+  if (lane == 0) s_max[wave] = m;
+  if (mode == kScanHist && A.hist)
+    for (int i = tid; i < kSampleBins; i += kSampleScan) s_hist[i] = 0;
+  if (tid == 0) s_len = 0;
+  __syncthreads();
+  m = s_max[0];
 #pragma unroll
-    for (int j = 0; j < L; ++j)
+  for (int i = 1; i < kSampleScan / 64; ++i) m = fmaxf(m, s_max[i]);
+  const int64_t at = (int64_t)r * A.segs + seg;
+  if (tid == 0) A.smax[at] = m;
+  if (mode == kScanMass) {
+    double s = 0.0;
+    if (m > -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) s += sample_weight(x[j][i], tm, p.c);
+      for (int j = 0; j < L; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s += sample_weight(x[j][i], m, p.c64);
+    }
+    s = wave_sum(s);
+    if (lane == 0) s_sum[wave] = s;
+    __syncthreads();
+    if (tid == 0) {
+      s = 0.0;
+      for (int i = 0; i < kSampleScan / 64; ++i) s += s_sum[i];
+      A.smass[at] = s;
+    }
+  } else if (mode == kScanHist && A.hist) {
+    const float top = floorf(m * p.cb);
+    int last = -1;
+    if (fabsf(top) < kSampleGrid) {                // false for -inf and NaN
+      const double scale = sample_scale(A.V);
+#pragma unroll
+      for (int j = 0; j < L; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float b = floorf(x[j][i] * p.cb);
+          const float d = top - b;
+          if (d < (float)(kSampleBins - 1)) {      // false for -inf
+            const double w = edge_weight(fma((double)x[j][i], p.c64, -((double)b + 1.0)));
+            atomicAdd(&s_hist[(int)d], (unsigned long long)rint(w * scale));
+            last = max(last, (int)d);
+          }
+        }
+    }
+    if (last >= 0) atomicMax(&s_len, last + 1);
+    __syncthreads();
+    const int len = s_len;
+    if (tid == 0) A.hlen[at] = len;
+    uint64_t* out = A.hist + at * kSampleBins;
+    for (int i = tid; i < len; i += kSampleScan) out[i] = s_hist[i];
   }
-  s = wave_add(s);
-  if (lane == 0) A.tmass[(int64_t)r * A.tiles + tile] = s;
 }
 
 // ---------------------------------------------------------------------------
@@ -209,70 +257,65 @@ __global__ __launch_bounds__(256) void sample_scan_kernel(SampleArgs A) {
 // ---------------------------------------------------------------------------
 struct SampleShared {
   uint64_t key[kSampleList];       // candidates: cand_key(z, id)
-  uint64_t aux[kSampleList];       // group lists; masses; keys by id
-  uint64_t hist[kSampleBins];
-  uint64_t wsum[16];
-  float wmax[16];
+  uint64_t aux[kSampleList];       // group lists; masses; keys by id; bin factors
+  uint64_t bins[kSampleBins];      // histograms; kept masses of the segments
+  uint64_t red[kSamplePick / 64];
+  uint64_t sub[kSampleSub];        // mass of the border's sub-bins
   int n, n2, pos;
-  uint64_t a, b;
+  uint64_t a;
 };
 
-__device__ __forceinline__ float block_max(SampleShared& s, float v) {
-  v = wave_max(v);
-  if ((threadIdx.x & 63) == 0) s.wmax[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = s.wmax[0];
-#pragma unroll
-  for (int i = 1; i < kSamplePick / 64; ++i) v = fmaxf(v, s.wmax[i]);
-  __syncthreads();
-  return v;
-}
-// Inclusive prefix sum over the block's threads; total in `total`.
-__device__ __forceinline__ uint64_t block_scan(SampleShared& s, uint64_t v, uint64_t& total) {
+// Inclusive prefix sum over the block's threads; their total in `total`.
+template <class T>
+__device__ __forceinline__ T block_scan(SampleShared& s, T v, T& total) {
   const int w = threadIdx.x >> 6;
   v = wave_incl_scan(v);
-  if ((threadIdx.x & 63) == 63) s.wsum[w] = v;
+  if ((threadIdx.x & 63) == 63) s.red[w] = __builtin_bit_cast(uint64_t, v);
   __syncthreads();
-  uint64_t add = 0, t = 0;
+  T add = 0, t = 0;
 #pragma unroll
   for (int i = 0; i < kSamplePick / 64; ++i) {
-    if (i < w) add += s.wsum[i];
-    t += s.wsum[i];
+    const T x = __builtin_bit_cast(T, s.red[i]);
+    if (i < w) add += x;
+    t += x;
   }
   __syncthreads();
   total = t;
-  return v + add;
+  return add + v;
 }
-__device__ __forceinline__ double block_sum(SampleShared& s, double v) {
-  v = wave_add(v);
-  if ((threadIdx.x & 63) == 0) s.wsum[threadIdx.x >> 6] = (uint64_t)__double_as_longlong(v);
+template <class T>
+__device__ __forceinline__ T block_total(SampleShared& s, T v) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) s.red[threadIdx.x >> 6] = __builtin_bit_cast(uint64_t, v);
   __syncthreads();
-  v = 0.0;
+  T t = 0;
 #pragma unroll
-  for (int i = 0; i < kSamplePick / 64; ++i) v += __longlong_as_double((long long)s.wsum[i]);
+  for (int i = 0; i < kSamplePick / 64; ++i) t += __builtin_bit_cast(T, s.red[i]);
   __syncthreads();
-  return v;
+  return t;
 }
 
-// The first position, in order, whose inclusive prefix of n values reaches
-// `target` >= 1 (-1: none), and the prefix before it; value(i) is called once
-// per position, in chunks of the block's size.
-template <class F>
-__device__ __forceinline__ int block_find(SampleShared& s, int n, uint64_t target, F value, uint64_t& before) {
-  uint64_t base = 0;
+// The first of n positions whose inclusive prefix reaches `target` > 0
+// (-1: none), and the prefix before it; value(i) is called once per position.
+template <class T, class F>
+__device__ __forceinline__ int block_find(SampleShared& s, int n, T target, F value, T& before) {
+  T base = 0;
   for (int i0 = 0; i0 < n; i0 += kSamplePick) {
     const int i = i0 + (int)threadIdx.x;
-    const uint64_t v = i < n ? value(i) : 0;
-    uint64_t total;
-    const uint64_t incl = base + block_scan(s, v, total);
+    const T v = i < n ? value(i) : 0;
+    T total;
+    const T incl = base + block_scan(s, v, total);
     if (base + total >= target) {                  // uniform
-      if (incl >= target && incl - v < target) {   // exactly one thread
-        s.pos = i;
-        s.a = incl - v;
-      }
+      // the lowest thread that reached it (rounding may make several doubles
+      // that did not grow look like the border: the lowest is taken)
+      if (threadIdx.x == 0) s.pos = 0x7fffffff;
       __syncthreads();
-      const int pos = s.pos;
-      before = s.a;
+      if (incl >= target) atomicMin(&s.pos, i);
+      __syncthreads();
+      const int pos = min(s.pos, n - 1);
+      if (i == pos) s.a = __builtin_bit_cast(uint64_t, incl - v);
+      __syncthreads();
+      before = __builtin_bit_cast(T, s.a);
       __syncthreads();
       return pos;
     }
@@ -290,13 +333,20 @@ __device__ __forceinline__ int pow2_at_least(int n) {
 __device__ __forceinline__ int key_id(uint64_t k) { return (int)(0xffffffffu - (uint32_t)k); }
 __device__ __forceinline__ float key_logit(uint64_t k) { return fkey_inv((uint32_t)(k >> 32)); }
 
-// Sort s.key[0, n) descending (padding to a power of two with zeros).
+// Sort key[0, n) descending (padding to a power of two with zeros).
 __device__ __forceinline__ void sort_keys(uint64_t* key, int n) {
   const int m = pow2_at_least(n);
   for (int i = n + (int)threadIdx.x; i < m; i += kSamplePick) key[i] = 0;
   __syncthreads();
   bitonic_desc(key, m);
 }
+
+__device__ __forceinline__ SampleShared& sample_shared() {
+  __shared__ SampleShared s;
+  return s;
+}
+template <class E>
+__device__ __attribute__((noinline)) void sample_stream_row(SampleArgs A, float m);
 
 template <class E>
 struct SamplePicker {
@@ -308,50 +358,63 @@ struct SamplePicker {
   const SampleRow p;
   const T* row;
   const float* gmax;
-  uint64_t* tsum;              // the row's tile sums (in place of its tile masses)
-  float m;
-  double scale;                // 2^s
+  float m, top;                // the largest logit and its bin on the grid
+  bool grid;                   // bins lie on the scan's grid
+  double scale;
 
-  __device__ SamplePicker(const SampleArgs& a, SampleShared& sh)
-      : A(a), s(sh), r(blockIdx.x), p(sample_row(a, blockIdx.x)), row((const T*)a.z + (int64_t)blockIdx.x * a.ldz),
-        gmax(a.gmax + (int64_t)blockIdx.x * a.groups), tsum((uint64_t*)(a.tmass + (int64_t)blockIdx.x * a.tiles)) {
-    int sh_bits = 62 - (32 - __clz(max(A.V - 1, 1)));
-    sh_bits = min(sh_bits, 52);
-    scale = (double)(1ull << sh_bits);
+  __device__ explicit SamplePicker(const SampleArgs& a)
+      : A(a), s(sample_shared()), r(blockIdx.x), p(sample_row(a, blockIdx.x)), row((const T*)a.z + (int64_t)blockIdx.x * a.ldz),
+        gmax(a.gmax + (int64_t)blockIdx.x * a.groups), scale(sample_scale(a.V)) {}
+
+  // Bin of a logit below the largest: non-decreasing as l falls.  The last
+  // bin has no mass.
+  __device__ __forceinline__ int bin(float l) const {
+    const float x = grid ? top - floorf(l * p.cb) : (m - l) * p.cb;
+    const int b = (int)fminf(x, (float)(kSampleBins - 1));   // NaN (inf * 0): the last bin
+    return l == m ? 0 : (l == -INFINITY ? kSampleBins - 1 : b);
   }
   __device__ __forceinline__ uint64_t mass(float l) const {
-    return sample_bin(l, m, p.cb) < kSampleBins - 1 ? (uint64_t)rint(sample_weight(l, m, p.c) * scale) : 0;
+    return bin(l) < kSampleBins - 1 ? (uint64_t)rint(sample_weight(l, m, p.c64) * scale) : 0;
   }
-  __device__ __forceinline__ double u() const {
-    return A.u_is_f64 ? ((const double*)A.u)[r] : (double)((const float*)A.u)[r];
+  // The mass if the id passes min_p, else 0.
+  __device__ __forceinline__ uint64_t kept_mass(float l) const {
+    const double w = sample_weight(l, m, p.c64);
+    return bin(l) < kSampleBins - 1 && w >= p.min_p ? (uint64_t)rint(w * scale) : 0;
+  }
+  __device__ __forceinline__ bool passes_min_p(float l) const {
+    return p.min_p == 0.0 || sample_weight(l, m, p.c64) >= p.min_p;
   }
   // The smallest inclusive prefix that exceeds u * total (1 .. total).
   __device__ __forceinline__ uint64_t draw_target(uint64_t total) const {
-    const double x = floor(u() * (double)total);
+    const double u = A.u_is_f64 ? ((const double*)A.u)[r] : (double)((const float*)A.u)[r];
+    const double x = floor(u * (double)total);
     if (!(x > 0.0)) return 1;                      // also a NaN
     return x >= (double)total ? total : min((uint64_t)x + 1, total);
   }
+  // One thread writes the result.
   __device__ __forceinline__ void emit(int id, float l, uint64_t total) const {
-    if (threadIdx.x == 0) {
-      A.token[r] = id;
-      // ln w of the drawn id minus the ln of the kept mass
-      if (A.logprob) A.logprob[r] = (float)((l == m ? 0.0 : ((double)l - (double)m) * p.c * 0.6931471805599453) -
-                                            log((double)total / scale));
-    }
+    A.token[r] = id;
+    // ln w of the drawn id minus the ln of the kept mass
+    if (A.logprob)
+      A.logprob[r] = (float)((l == m ? 0.0 : ((double)l - (double)m) * p.c64 * (1.0 / 64.0)) - log((double)total / scale));
   }
 
   // Lowest id of the largest logit.
-  __device__ void pick_greedy() {
-    int g = A.groups;
+  __device__ __forceinline__ void pick_greedy() {
+    if (threadIdx.x == 0) s.pos = A.groups;
+    __syncthreads();
     for (int i = threadIdx.x; i < A.groups; i += kSamplePick)
-      if (gmax[i] == m) { g = i; break; }
-    g = (int)-block_max(s, -(float)g);             // < 2^24: exact
+      if (gmax[i] == m) {
+        atomicMin(&s.pos, i);
+        break;
+      }
+    __syncthreads();
     if (threadIdx.x < 64) {
-      const int v = g * kSampleGroup + (int)threadIdx.x;
+      const int v = s.pos * kSampleGroup + (int)threadIdx.x;
       const bool hit = v < A.V && sample_logit(load_elem<E>(row + v)) == m;
       const unsigned long long b = __ballot(hit);
       if (threadIdx.x == 0) {
-        A.token[r] = g * kSampleGroup + (int)__builtin_ctzll(b);
+        A.token[r] = s.pos * kSampleGroup + (int)__builtin_ctzll(b);
         if (A.logprob) A.logprob[r] = 0.f;
       }
     }
@@ -359,25 +422,29 @@ struct SamplePicker {
 
   // Bin that `want` groups have their maxima in or above (the last one with
   // mass if there are fewer).
-  __device__ int group_bin(int want) {
-    for (int i = threadIdx.x; i < kSampleBins; i += kSamplePick) s.hist[i] = 0;
+  __device__ __forceinline__ int group_bin(int want) {
+    int* cnt = (int*)s.bins;
+    for (int i = threadIdx.x; i < kSampleBins; i += kSamplePick) cnt[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < A.groups; i += kSamplePick)
-      atomicAdd((unsigned long long*)&s.hist[sample_bin(gmax[i], m, p.cb)], 1ull);
+    for (int i = threadIdx.x; i < A.groups; i += kSamplePick) atomicAdd(&cnt[bin(gmax[i])], 1);
     __syncthreads();
     uint64_t before;
-    const int b = block_find(s, kSampleBins - 1, (uint64_t)want, [&](int i) { return s.hist[i]; }, before);
-    return b < 0 ? kSampleBins - 2 : b;
+    // two bins per thread: one prefix sum covers them all
+    const int b = block_find(
+        s, kSampleBins / 2, (uint64_t)want,
+        [&](int i) -> uint64_t { return cnt[2 * i] + (2 * i + 1 < kSampleBins - 1 ? cnt[2 * i + 1] : 0); }, before);
+    if (b < 0) return kSampleBins - 2;
+    return before + cnt[2 * b] >= (uint64_t)want ? 2 * b : 2 * b + 1;
   }
 
   // All ids in bins <= b into s.key (unordered); their number, or a number
   // past kSampleList if they do not fit.
-  __device__ int gather(int b) {
+  __device__ __forceinline__ int gather(int b) {
     int* list = (int*)s.aux;                       // groups to read: 2 * kSampleList places
     if (threadIdx.x == 0) s.n = s.n2 = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < A.groups; i += kSamplePick)
-      if (sample_bin(gmax[i], m, p.cb) <= b) {
+      if (bin(gmax[i]) <= b) {
         const int at = atomicAdd(&s.n2, 1);
         if (at < 2 * kSampleList) list[at] = i;
       }
@@ -395,68 +462,323 @@ struct SamplePicker {
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (v[j] < A.V && sample_bin(x[j], m, p.cb) <= b) {
+        if (v[j] < A.V && bin(x[j]) <= b) {
           const int at = atomicAdd(&s.n, 1);
           if (at < kSampleList) s.key[at] = cand_key(x[j], (uint32_t)v[j]);
         }
     }
     __syncthreads();
-    return s.n;
+    const int n = s.n;
+    __syncthreads();                               // the caller may clear it
+    return n;
   }
 
-  // Draw from the list's first n entries whose mass counts: sort by id, find.
-  // keep(i) says whether entry i of s.key is kept.
-  template <class F>
-  __device__ void draw_list(int n, F keep) {
-    // aux: (~id, position) keys, largest first = lowest id first
+  // Draw from the n <= kSampleRank ids of s.key (any order), by counting: per
+  // id, how many stand before it and with what mass.  All prefixes are sums
+  // over the list, split over the block's threads and joined with integer
+  // atomics.  row_mass: the mass that top_p is a share of when top_k is off.
+  __device__ __forceinline__ void draw_few(int n, double row_mass) {
+    uint64_t* wt = s.aux;                          // masses
+    uint64_t* pre = s.aux + kSampleRank;           // mass before, by rank; then inclusive mass, by id
+    int* rank = (int*)(s.aux + 2 * kSampleRank);
+    const int tid = threadIdx.x, i = tid & (kSampleRank - 1), q = tid / kSampleRank;
+    constexpr int Q = kSamplePick / kSampleRank;
+    uint64_t k = 0, w = 0;
+    if (i < n) {
+      k = s.key[i];
+      w = mass(key_logit(k));
+    }
+    if (q == 0) {
+      wt[i] = w;
+      pre[i] = 0;
+      rank[i] = 0;
+    }
+    __syncthreads();
+    if (i < n) {
+      int c = 0;
+      uint64_t a = 0;
+      for (int j = q; j < n; j += Q)
+        if (s.key[j] > k) {
+          ++c;
+          a += wt[j];
+        }
+      atomicAdd(&rank[i], c);
+      atomicAdd((unsigned long long*)&pre[i], (unsigned long long)a);
+    }
+    __syncthreads();
+    bool keep = i < n && (p.top_k == 0 || rank[i] < p.top_k);
+    if (p.top_p < 1.0) {
+      const double all = p.top_k > 0 ? (double)block_total(s, q == 0 && keep ? w : (uint64_t)0) : row_mass;
+      keep = keep && (rank[i] == 0 || (double)pre[i] < p.top_p * all);
+    }
+    keep = keep && w > 0 && passes_min_p(key_logit(k));
+    __syncthreads();
+    if (q == 0) {
+      wt[i] = keep ? w : 0;
+      pre[i] = 0;
+    }
+    const uint64_t total = block_total(s, q == 0 && keep ? w : (uint64_t)0);   // its barriers order the writes
+    if (keep) {
+      uint64_t a = 0;
+      for (int j = q; j < n; j += Q)
+        if ((uint32_t)s.key[j] >= (uint32_t)k) a += wt[j];       // ids <= this one
+      atomicAdd((unsigned long long*)&pre[i], (unsigned long long)a);
+    }
+    __syncthreads();
+    const uint64_t want = draw_target(total);
+    if (q == 0 && keep && pre[i] >= want && pre[i] - w < want) emit(key_id(k), key_logit(k), total);
+  }
+
+  // Draw from the first n entries of s.key that pass min_p: sorted by id.
+  __device__ __forceinline__ void draw_list(int n) {
+    // aux: (~id, position) keys, largest first = lowest id first; entries
+    // that are not kept are zero and sort last
     for (int i = threadIdx.x; i < n; i += kSamplePick)
-      s.aux[i] = keep(i) ? (((uint64_t)(uint32_t)s.key[i]) << 32) | (uint32_t)i : 0;
+      s.aux[i] = passes_min_p(key_logit(s.key[i])) ? (((uint64_t)(uint32_t)s.key[i]) << 32) | (uint32_t)i : 0;
     __syncthreads();
     sort_keys(s.aux, n);
-    // entries that are not kept sort last with key 0 and have no mass
     auto value = [&](int i) -> uint64_t {
       const uint64_t a = s.aux[i];
       return a ? mass(key_logit(s.key[(uint32_t)a])) : 0;
     };
-    uint64_t total = 0, before;
-    for (int i0 = 0; i0 < n; i0 += kSamplePick) {
-      const int i = i0 + (int)threadIdx.x;
-      uint64_t t;
-      block_scan(s, i < n ? value(i) : 0, t);
-      total += t;
-    }
+    uint64_t part = 0, before;
+    for (int i = threadIdx.x; i < n; i += kSamplePick) part += value(i);
+    const uint64_t total = block_total(s, part);
     const int at = block_find(s, n, draw_target(total), value, before);
     const uint64_t k = s.key[(uint32_t)s.aux[max(at, 0)]];
-    emit(key_id(k), key_logit(k), total);
+    if (threadIdx.x == 0) emit(key_id(k), key_logit(k), total);
   }
 
-  // Mass of the whole row, in units of 1 / scale, from the scan's tile masses
-  // (each relative to its tile's own largest logit).
-  __device__ double tile_mass(int i) const {
-    float tm = -INFINITY;
-    const int g0 = i * (kSampleTile / kSampleGroup);
-    for (int g = g0; g < min(g0 + kSampleTile / kSampleGroup, A.groups); ++g) tm = fmaxf(tm, gmax[g]);
-    if (!(tm > -INFINITY)) return 0.0;
-    return __longlong_as_double((long long)tsum[i]) * sample_weight(tm, m, p.c) * scale;
+  // Draw from a list that holds every id in bins <= some bin, and so every
+  // kept one.
+  __device__ __forceinline__ void pick_list(int n, double row_mass) {
+    if (n <= kSampleRank) return draw_few(n, row_mass);
+    int n1 = n;
+    if (p.top_k > 0 || p.top_p < 1.0) {
+      sort_keys(s.key, n);
+      if (p.top_k > 0) n1 = min(n, p.top_k);
+    }
+    if (p.top_p < 1.0) {
+      auto value = [&](int i) { return mass(key_logit(s.key[i])); };
+      double all = row_mass;
+      if (p.top_k > 0) {
+        uint64_t part = 0;
+        for (int i = threadIdx.x; i < n1; i += kSamplePick) part += value(i);
+        all = (double)block_total(s, part);
+      }
+      uint64_t before;
+      const int at = block_find(s, n1, (uint64_t)fmax(ceil(p.top_p * all), 1.0), value, before);
+      if (at >= 0) n1 = at + 1;
+    }
+    draw_list(n1);
   }
 
-  // ---- rows whose kept set has no short list -------------------------------
-  // Calls f(id, logit) for every id of the row, each thread a strided share.
+  // ---- flat rows, from the scan's histograms -------------------------------
+  // Mass of bin j of the row relative to the largest logit: its entries are
+  // kept relative to the bin's upper edge, top - j + 1 on the grid.
+  __device__ __forceinline__ double bin_factor(int j) const {
+    return exp(fma((double)m, -p.c64, (double)top - (double)j + 1.0) * (1.0 / 64.0));
+  }
+  __device__ __forceinline__ int seg_offset(int sg) const {
+    // bins between the row's largest logit and the segment's
+    const float b = top - floorf(A.smax[(int64_t)r * A.segs + sg] * p.cb);
+    return (int)fminf(b, (float)kSampleBins);      // -inf: outside
+  }
+
+  // The kept set is every id in bins < lo and, in bins lo..hi, those with
+  // cand_key >= lim.
+  struct Kept {
+    int lo, hi;
+    uint64_t lim;
+  };
+  __device__ __forceinline__ bool is_kept(const Kept& k, int v, float l) const {
+    const int b = bin(l);
+    return v < A.V && b < kSampleBins - 1 && (b < k.lo || (b <= k.hi && cand_key(l, (uint32_t)v) >= k.lim));
+  }
+
+  // Draw, given the segments' kept masses in s.bins.  A segment whose mass
+  // is less than the rounding of its ids' (none of them has a unit) is left
+  // out and the draw repeated; the largest logit's segment always stays.
+  __device__ __forceinline__ void draw_segment(const Kept& k) {
+    while (!try_segment(k)) {}
+  }
+  __device__ __forceinline__ bool try_segment(const Kept& k) {
+    uint64_t part = 0, before = 0;
+    for (int i = threadIdx.x; i < A.segs; i += kSamplePick) part += s.bins[i];
+    const uint64_t total = block_total(s, part);
+    const uint64_t want = draw_target(total);
+    const int sg = max(block_find(s, A.segs, want, [&](int i) { return s.bins[i]; }, before), 0);
+    // 16 consecutive ids per thread
+    constexpr int C = kSampleSeg / kSamplePick;
+    const int v0 = sg * kSampleSeg + (int)threadIdx.x * C;
+    float x[C];
+    uint64_t sum = 0;
+#pragma unroll
+    for (int j = 0; j < C / N; ++j) sample_load<E>(row, v0 + j * N, A.V, x + j * N);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      if (!is_kept(k, v0 + i, x[i])) x[i] = -INFINITY;
+      sum += kept_mass(x[i]);
+    }
+    uint64_t all;
+    uint64_t run = block_scan(s, sum, all) - sum;
+    if (all == 0) {
+      if (threadIdx.x == 0) s.bins[sg] = 0;
+      __syncthreads();
+      return false;
+    }
+    // (a segment's mass taken from its histogram may differ from this sum in
+    // the last units: the target is held inside it)
+    const uint64_t aim = min(want > before ? want - before : (uint64_t)1, all);
+    if (run < aim && run + sum >= aim) {           // one thread
+#pragma unroll 1
+      for (int i = 0; i < C; ++i) {
+        const float l = sample_logit(load_elem<E>(row + min(v0 + i, A.V - 1)));
+        const uint64_t w = v0 + i < A.V && is_kept(k, v0 + i, l) ? kept_mass(l) : 0;
+        run += w;
+        if (w && run >= aim) {
+          emit(v0 + i, l, total);
+          break;
+        }
+      }
+    }
+    return true;
+  }
+
+  // top_p and min_p without top_k: the row's histogram into s.bins; returns
+  // the mass of the row, and the bins lo .. hi that the kept set ends in.
+  __device__ __forceinline__ double join_hist(int& lo, int& hi) {
+    const int64_t at0 = (int64_t)r * A.segs;
+    double* bm = (double*)s.bins;
+    // per segment: where its histogram starts among the row's bins, its length
+    int2* seg = (int2*)s.aux;
+    for (int sg = threadIdx.x; sg < A.segs; sg += kSamplePick) seg[sg] = make_int2(seg_offset(sg), A.hlen[at0 + sg]);
+    __syncthreads();
+    double part = 0.0;
+    for (int j = threadIdx.x; j < kSampleBins; j += kSamplePick) {
+      uint64_t a = 0;
+#pragma unroll 8
+      for (int sg = 0; sg < A.segs; ++sg) {
+        const int i = j - seg[sg].x;
+        a += i >= 0 && i < seg[sg].y ? A.hist[(at0 + sg) * kSampleBins + i] : 0;
+      }
+      const double v = a && j < kSampleBins - 1 ? (double)a * bin_factor(j) : 0.0;
+      bm[j] = v;
+      part += v;
+    }
+    const double all = block_total(s, part);       // (orders the writes)
+    const double need = p.top_p * all;
+    lo = kSampleBins - 1;
+    hi = kSampleBins - 2;
+    if (p.min_p > 0.0) {
+      // w >= min_p: at most x bins below the largest logit; a bin's ids lie
+      // within one bin of its number, and one more for rounding
+      const double x = fmin(-64.0 * log(p.min_p), (double)(2 * kSampleBins));
+      lo = min(max((int)x - 1, 0), lo);
+      hi = min((int)x + 2, hi);
+    }
+    if (p.top_p < 1.0) {
+      double before;
+      const int b = block_find(s, kSampleBins / 2, need, [&](int i) { return bm[2 * i] + bm[2 * i + 1]; }, before);
+      const int jb = b < 0 ? kSampleBins - 2 : (before + bm[2 * b] >= need ? 2 * b : 2 * b + 1);
+      lo = min(lo, jb);
+      hi = min(hi, jb);
+    }
+    return all;
+  }
+
+  // The kept set of a flat row, given its histogram in s.bins, and the
+  // segments' kept masses in its place.  False: the border holds too many ids.
+  __device__ __forceinline__ bool cut_hist(double all, int lo, int hi, Kept& k) {
+    const int64_t at0 = (int64_t)r * A.segs;
+    const double* bm = (const double*)s.bins;
+    const double need = p.top_p * all;
+    // the border's ids: on the grid, bins lo .. hi are lb <= l cb < ub
+    if (threadIdx.x == 0) s.n = s.n2 = 0;
+    for (int i = threadIdx.x; i < kSampleSub; i += kSamplePick) s.sub[i] = 0;
+    double part = 0.0;
+    for (int j = threadIdx.x; j < lo; j += kSamplePick) part += bm[j];
+    const double above = block_total(s, part);     // (orders the writes above)
+    const float lb = top - (float)hi, ub = top - (float)lo + 1.f;
+    const float per = (float)kSampleSub / (float)(hi - lo + 1);
+    for_row([&](int v, float l) {
+      const float t = l * p.cb;
+      if (t >= lb && t < ub) {
+        const int at = atomicAdd(&s.n, 1);
+        if (at < kSampleList) s.key[at] = cand_key(l, (uint32_t)v);
+        if (p.top_p < 1.0) atomicAdd((unsigned long long*)&s.sub[min((int)((ub - t) * per), kSampleSub - 1)], (unsigned long long)mass(l));
+      }
+    });
+    __syncthreads();
+    const int n = s.n;
+    __syncthreads();
+    if (n > kSampleList) return false;
+    // which of them stay: those that pass min_p and, with top_p, the whole
+    // sub-bins above the one where their mass reaches its share, and of that
+    // one's ids, sorted, the first
+    uint64_t lim = 0;
+    if (p.top_p < 1.0) {
+      if (need <= above && lo > 0) {
+        lim = ~0ull;
+      } else {
+        const uint64_t want = (uint64_t)fmax(ceil(need - above), 1.0);
+        uint64_t before;
+        const int sb = block_find(s, kSampleSub, want, [&](int i) { return s.sub[i]; }, before);
+        if (sb >= 0) {
+          for (int i = threadIdx.x; i < n; i += kSamplePick) {
+            const float t = key_logit(s.key[i]) * p.cb;
+            if (min((int)((ub - t) * per), kSampleSub - 1) == sb) s.aux[atomicAdd(&s.n2, 1)] = s.key[i];
+          }
+          __syncthreads();
+          const int ns = s.n2;
+          __syncthreads();
+          sort_keys(s.aux, ns);
+          const int at = block_find(s, ns, want - before, [&](int i) { return mass(key_logit(s.aux[i])); }, before);
+          lim = s.aux[at < 0 ? ns - 1 : at];
+          __syncthreads();
+        }
+      }
+    }
+    k = Kept{lo, hi, lim};
+    // the segments' masses above the border, a wave per segment, then the
+    // border's kept ids
+    double* fac = (double*)s.aux;
+    for (int j = threadIdx.x; j < lo; j += kSamplePick) fac[j] = bin_factor(j);
+    __syncthreads();
+    for (int sg = threadIdx.x >> 6; sg < A.segs; sg += kSamplePick / 64) {
+      const int off = seg_offset(sg), len = min(A.hlen[at0 + sg], lo - off);
+      const uint64_t* h = A.hist + (at0 + sg) * kSampleBins;
+      double v = 0.0;
+#pragma unroll 8
+      for (int i = threadIdx.x & 63; i < len; i += 64) v += (double)h[i] * fac[off + i];
+      v = wave_sum(v);
+      if ((threadIdx.x & 63) == 0) s.bins[sg] = (uint64_t)rint(v);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kSamplePick) {
+      const uint64_t c = s.key[i];
+      const uint64_t w = c >= lim ? kept_mass(key_logit(c)) : 0;
+      if (w) atomicAdd((unsigned long long*)&s.bins[key_id(c) / kSampleSeg], (unsigned long long)w);
+    }
+    __syncthreads();
+    return true;
+  }
+
+  // ---- rows that are streamed several times --------------------------------
+  // Calls f(id, logit) for every id of the row above -inf, each thread a
+  // strided share.
   template <class F>
   __device__ __forceinline__ void for_row(F f) {
-    for (int v = (int)threadIdx.x * N; v < A.V; v += kSamplePick * N * 2) {
-      float x[2][N];
-      const int v2 = v + kSamplePick * N;
-      sample_load<E>(row, v, A.V, x[0]);
-      if (v2 < A.V) sample_load<E>(row, v2, A.V, x[1]);
+    constexpr int D = 32 / N;                      // loads in flight
+    for (int v = (int)threadIdx.x * N; v < A.V; v += kSamplePick * N * D) {
+      float x[D][N];
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (v + i < A.V) f(v + i, x[0][i]);
-      if (v2 < A.V) {
+      for (int j = 0; j < D; ++j) sample_load<E>(row, v + j * kSamplePick * N, A.V, x[j]);
+#pragma unroll
+      for (int j = 0; j < D; ++j)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (v2 + i < A.V) f(v2 + i, x[1][i]);
-      }
+          if (x[j][i] > -INFINITY) f(v + j * kSamplePick * N + i, x[j][i]);
     }
   }
 
@@ -464,31 +786,27 @@ struct SamplePicker {
   // descending order, of the kept ids with mass whose count (MASS false) or
   // mass reaches a target; target(total) gives it from their total.
   template <bool MASS, class F>
-  __device__ uint64_t cut(uint64_t lim, F target) {
-    for (int i = threadIdx.x; i < kSampleBins; i += kSamplePick) s.hist[i] = 0;
+  __device__ __forceinline__ uint64_t cut(uint64_t lim, F target) {
+    for (int i = threadIdx.x; i < kSampleBins; i += kSamplePick) s.bins[i] = 0;
     __syncthreads();
     for_row([&](int v, float l) {
-      const int b = sample_bin(l, m, p.cb);
+      const int b = bin(l);
       if (b < kSampleBins - 1 && cand_key(l, (uint32_t)v) >= lim)
-        atomicAdd((unsigned long long*)&s.hist[b], MASS ? (unsigned long long)mass(l) : 1ull);
+        atomicAdd((unsigned long long*)&s.bins[b], MASS ? (unsigned long long)mass(l) : 1ull);
     });
     __syncthreads();
-    uint64_t total = 0;
-    for (int i0 = 0; i0 < kSampleBins; i0 += kSamplePick) {
-      uint64_t t;
-      block_scan(s, s.hist[i0 + threadIdx.x], t);
-      total += t;
-    }
-    const uint64_t want = target(total);
+    uint64_t part = 0;
+    for (int i = threadIdx.x; i < kSampleBins; i += kSamplePick) part += s.bins[i];
+    const uint64_t want = target(block_total(s, part));
     uint64_t before;
-    const int b = block_find(s, kSampleBins - 1, want, [&](int i) { return s.hist[i]; }, before);
+    const int b = block_find(s, kSampleBins - 1, want, [&](int i) { return s.bins[i]; }, before);
     if (b < 0) return lim;                         // the target is not reached: all stay
     const uint64_t rest = want - before;
     if (threadIdx.x == 0) s.n = 0;
     __syncthreads();
     for_row([&](int v, float l) {
       const uint64_t k = cand_key(l, (uint32_t)v);
-      if (sample_bin(l, m, p.cb) == b && k >= lim) {
+      if (bin(l) == b && k >= lim) {
         const int at = atomicAdd(&s.n, 1);
         if (at < kSampleList) s.key[at] = k;
       }
@@ -508,89 +826,57 @@ struct SamplePicker {
     // key at the border digit by digit, a pass over the row per digit
     uint64_t prefix = 0, mask = 0, left = rest;
     for (int shift = 56; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kSamplePick) s.hist[i] = 0;
+      for (int i = threadIdx.x; i < 256; i += kSamplePick) s.bins[i] = 0;
       __syncthreads();
       for_row([&](int v, float l) {
         const uint64_t k = cand_key(l, (uint32_t)v);
-        if (sample_bin(l, m, p.cb) == b && k >= lim && (k & mask) == prefix)
-          atomicAdd((unsigned long long*)&s.hist[255 - ((k >> shift) & 255)], MASS ? (unsigned long long)mass(l) : 1ull);
+        if (bin(l) == b && k >= lim && (k & mask) == prefix)
+          atomicAdd((unsigned long long*)&s.bins[255 - ((k >> shift) & 255)], MASS ? (unsigned long long)mass(l) : 1ull);
       });
       __syncthreads();
-      const int at = block_find(s, 256, left, [&](int i) { return s.hist[i]; }, before);
+      const int at = block_find(s, 256, left, [&](int i) { return s.bins[i]; }, before);
       prefix |= (uint64_t)(255 - max(at, 0)) << shift;
       mask |= 255ull << shift;
-      left -= before;
+      left -= min(before, left - 1);
       __syncthreads();
     }
     return prefix;
   }
 
-  // Draw from the ids with cand_key >= lim and w >= min_p, whose masses per
-  // tile are in tsum (already, or counted here).
-  __device__ void draw_row(uint64_t lim, bool counted) {
-    const int lane = threadIdx.x & 63;
-    auto kept = [&](int v, float l) -> uint64_t {
-      if (v >= A.V || cand_key(l, (uint32_t)v) < lim) return 0;
-      if (p.min_p > 0.0 && !(sample_weight(l, m, p.c) >= p.min_p)) return 0;
-      return mass(l);
-    };
-    if (!counted) {
-      for (int t = threadIdx.x >> 6; t < A.tiles; t += kSamplePick / 64) {
-        uint64_t a = 0;
+  __device__ __forceinline__ void pick_stream() {
+    uint64_t lim = 0;
+    if (p.top_k > 0) lim = cut<false>(lim, [&](uint64_t) { return (uint64_t)p.top_k; });
+    if (p.top_p < 1.0)
+      lim = cut<true>(lim, [&](uint64_t total) { return (uint64_t)fmax(ceil(p.top_p * (double)total), 1.0); });
+    const Kept k{0, kSampleBins - 1, lim};
+    for (int i = threadIdx.x; i < A.segs; i += kSamplePick) s.bins[i] = 0;
+    __syncthreads();
+    // a wave's ids of one vector lie in one segment (64 * N divides it)
+    for (int v = (int)threadIdx.x * N; v < (A.V + kSampleSeg - 1) / kSampleSeg * kSampleSeg; v += kSamplePick * N) {
+      float x[N];
+      sample_load<E>(row, v, A.V, x);
+      uint64_t a = 0;
 #pragma unroll
-        for (int j = 0; j < 16 / N; ++j) {
-          float x[N];
-          const int v = t * kSampleTile + j * 64 * N + lane * N;
-          sample_load<E>(row, v, A.V, x);
-#pragma unroll
-          for (int i = 0; i < N; ++i) a += kept(v + i, x[i]);
-        }
-        a = wave_add(a);
-        if (lane == 0) tsum[t] = a;
-      }
-      __syncthreads();
+      for (int i = 0; i < N; ++i)
+        if (is_kept(k, v + i, x[i])) a += kept_mass(x[i]);
+      a = wave_sum(a);
+      if ((threadIdx.x & 63) == 0 && a) atomicAdd((unsigned long long*)&s.bins[v / kSampleSeg], (unsigned long long)a);
     }
-    uint64_t total = 0, before = 0;
-    for (int i0 = 0; i0 < A.tiles; i0 += kSamplePick) {
-      const int i = i0 + (int)threadIdx.x;
-      uint64_t t;
-      block_scan(s, i < A.tiles ? tsum[i] : 0, t);
-      total += t;
-    }
-    const uint64_t want = draw_target(total);
-    const int tile = block_find(s, A.tiles, want, [&](int i) { return tsum[i]; }, before);
-    if (tile < 0 || threadIdx.x >= 64) return;
-    // inside the tile: 16 consecutive ids per lane
-    uint64_t w[16], a = 0;
-    const int v0 = tile * kSampleTile + lane * 16;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int v = v0 + i;
-      const float l = v < A.V ? sample_logit(load_elem<E>(row + v)) : -INFINITY;
-      w[i] = kept(v, l);
-      a += w[i];
-    }
-    const uint64_t incl = wave_incl_scan(a);
-    uint64_t run = before + incl - a;
-    int found = -1, last = -1;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      run += w[i];
-      if (w[i]) last = v0 + i;
-      if (found < 0 && run >= want && w[i]) found = v0 + i;
-    }
-    // the lowest lane that reached it; if rounding of the tile's mass left
-    // none, the tile's last id with mass
-    const unsigned long long hit = __ballot(found >= 0), any = __ballot(last >= 0);
-    const int src = hit ? (int)__builtin_ctzll(hit) : (any ? 63 - (int)__builtin_clzll(any) : 0);
-    const int id = __shfl(hit ? found : last, src);
-    if (id >= 0) emit(id, sample_logit(load_elem<E>(row + id)), total);
+    __syncthreads();
+    draw_segment(k);
   }
 
-  __device__ void pick() {
-    float x = -INFINITY;
-    for (int i = threadIdx.x; i < A.groups; i += kSamplePick) x = fmaxf(x, gmax[i]);
-    m = block_max(s, x);
+  __device__ __forceinline__ void set_max(float largest) {
+    m = largest;
+    top = floorf(m * p.cb);
+    grid = fabsf(top) < kSampleGrid - 2 * kSampleBins;
+  }
+
+  __device__ __forceinline__ void pick() {
+    const float* smax = A.smax + (int64_t)r * A.segs;
+    m = -INFINITY;
+    for (int i = threadIdx.x & 63; i < A.segs; i += 64) m = fmaxf(m, smax[i]);
+    m = wave_max(m);                               // every wave the same
     if (m == -INFINITY) {                          // nothing to draw from
       if (threadIdx.x == 0) {
         A.token[r] = -1;
@@ -599,73 +885,52 @@ struct SamplePicker {
       return;
     }
     if (p.greedy) return pick_greedy();
-    const bool filtered = p.top_k > 0 || p.top_p < 1.0 || p.min_p > 0.0;
-    if (!filtered) {
-      for (int i = threadIdx.x; i < A.tiles; i += kSamplePick) tsum[i] = (uint64_t)rint(tile_mass(i));
-      __syncthreads();
-      return draw_row(0, true);
-    }
-    double row_mass = 0.0;
-    if (sample_needs_mass(p)) {
-      for (int i = threadIdx.x; i < A.tiles; i += kSamplePick) row_mass += tile_mass(i);
-      row_mass = block_sum(s, row_mass);
-    }
-    // how deep the list must go
-    int b = kSampleBins - 2;
-    if (p.top_k > 0) b = group_bin(p.top_k);
-    else if (p.top_p < 1.0) b = group_bin(kSampleTopGroups);
-    // (top_p of top_k's ids needs the mass of all of them)
-    if (p.min_p > 0.0 && !(p.top_k > 0 && p.top_p < 1.0)) b = min(b, (int)fmin(-64.0 * log(p.min_p) + 2.0, (double)(kSampleBins - 2)));
-    const int n = gather(b);
-    if (n <= kSampleList) {
-      if (p.top_k == 0 && p.top_p == 1.0)
-        return draw_list(n, [&](int i) { return sample_weight(key_logit(s.key[i]), m, p.c) >= p.min_p; });
-      sort_keys(s.key, n);
-      const int n1 = p.top_k > 0 ? min(n, p.top_k) : n;
-      int n2 = n1;
-      bool whole = true;
-      if (p.top_p < 1.0) {
-        double all = row_mass;
-        auto value = [&](int i) { return mass(key_logit(s.key[i])); };
-        uint64_t total = 0, before;
-        for (int i0 = 0; i0 < n1; i0 += kSamplePick) {
-          const int i = i0 + (int)threadIdx.x;
-          uint64_t t;
-          block_scan(s, i < n1 ? value(i) : 0, t);
-          total += t;
-        }
-        if (p.top_k > 0) all = (double)total;
-        const double need = fmax(ceil(p.top_p * all), 1.0);
-        whole = p.top_k > 0 || (double)total >= need || b == kSampleBins - 2 || cut_by_min_p(b);
-        if (whole) {
-          const int at = block_find(s, n1, (uint64_t)need, value, before);
-          n2 = at < 0 ? n1 : at + 1;
-        }
+    set_max(m);
+    const int mode = sample_scan_mode(A, p);
+    Kept k{0, kSampleBins - 1, 0};
+    if (mode == kScanMass) {
+      for (int i = threadIdx.x; i < A.segs; i += kSamplePick) {
+        const double v = A.smass[(int64_t)r * A.segs + i];
+        s.bins[i] = v > 0.0 ? (uint64_t)rint(v * sample_weight(smax[i], m, p.c64) * scale) : 0;
       }
-      if (whole)
-        return draw_list(n2, [&](int i) {
-          return p.min_p == 0.0 || sample_weight(key_logit(s.key[i]), m, p.c) >= p.min_p;
-        });
+      __syncthreads();
+    } else {
+      // how deep the kept ids can lie
+      const bool hist = mode == kScanHist && A.hist;
+      if (hist && !grid) return sample_stream_row<E>(A, m);
+      double all = 0.0;
+      int lo = 0, hi = kSampleBins - 2;
+      if (hist) all = join_hist(lo, hi);
+      else if (p.top_k > 0) hi = group_bin(p.top_k);
+      // (top_p of top_k's ids needs the mass of all of them)
+      if (!hist && p.min_p > 0.0 && p.top_p == 1.0)
+        hi = min(hi, (int)fmin(-64.0 * log(p.min_p) + 3.0, (double)(kSampleBins - 2)));
+      const int n = gather(hi);
+      if (n <= kSampleList) {
+        if (!hist && p.top_k == 0 && p.top_p < 1.0) {
+          uint64_t part = 0;
+          for (int i = threadIdx.x; i < n; i += kSamplePick) part += mass(key_logit(s.key[i]));
+          all = (double)block_total(s, part);
+        }
+        return pick_list(n, all);
+      }
+      if (!hist || !cut_hist(all, lo, hi, k)) return sample_stream_row<E>(A, m);
     }
-    // the kept set by streaming the row
-    uint64_t lim = 0;
-    if (p.top_k > 0) lim = cut<false>(lim, [&](uint64_t) { return (uint64_t)p.top_k; });
-    if (p.top_p < 1.0)
-      lim = cut<true>(lim, [&](uint64_t total) { return (uint64_t)fmax(ceil(p.top_p * (double)total), 1.0); });
-    draw_row(lim, false);
-  }
-
-  // The list holds every id that min_p keeps (and more): what top_p would
-  // keep beyond it falls to min_p anyway.
-  __device__ __forceinline__ bool cut_by_min_p(int b) const {
-    return p.min_p > 0.0 && b >= (int)fmin(-64.0 * log(p.min_p) + 2.0, (double)(kSampleBins - 2));
+    draw_segment(k);
   }
 };
 
+// The rare path, kept out of the kernel's registers.
+template <class E>
+__device__ void sample_stream_row(SampleArgs A, float m) {
+  SamplePicker<E> pick(A);
+  pick.set_max(m);
+  pick.pick_stream();
+}
+
 template <class E>
 __global__ __launch_bounds__(kSamplePick) void sample_pick_kernel(SampleArgs A) {
-  __shared__ SampleShared s;
-  SamplePicker<E> pick(A, s);
+  SamplePicker<E> pick(A);
   pick.pick();
 }
 
