@@ -27,14 +27,16 @@
 //  - finds from the group maxima (top_k) or from the joined histogram how far
 //    below the largest logit kept ids can lie;
 //  - when few ids lie that high, reads back only their 64-id groups and ranks
-//    them (up to 256 by counting, more by sorting);
+//    them (up to 256 by counting; of a top_k, up to 4096 by sorting);
 //  - otherwise (a flat row) reads the row once more for the ids of the border
 //    bin alone: the bins above it are kept whole, and the segments' kept
 //    masses come from their histograms, so only one segment is looked into.
-// Rows that neither suits (more than 4096 equal logits at the border, top_k
-// past the list, temperatures that put the grid beyond 2^22 bins) stream the
-// row several times.
+// Rows that neither suits (more than 4096 ids in the border bin, equal logits
+// mostly; top_k past the list; temperatures that put the grid beyond 2^22
+// bins) stream the row several times.
 #pragma once
+
+#include <type_traits>
 
 #include "kd_layout.hpp"
 #include "kd_order.hpp"
@@ -265,34 +267,33 @@ struct SampleShared {
   uint64_t a;
 };
 
+// The sixteen waves' values, prefix-summed by every wave for itself: lane i
+// of its first sixteen holds the sum of waves 0 .. i.
+template <class T>
+__device__ __forceinline__ T waves_scan(SampleShared& s, T v) {
+  static_assert(kSamplePick == 1024, "sixteen waves");
+  if ((threadIdx.x & 63) == 63) s.red[threadIdx.x >> 6] = __builtin_bit_cast(uint64_t, v);
+  __syncthreads();
+  T t = __builtin_bit_cast(T, s.red[threadIdx.x & 15]);
+  t += dpp<0x111>(t);
+  t += dpp<0x112>(t);
+  t += dpp<0x114>(t);
+  t += dpp<0x118>(t);
+  __syncthreads();
+  return t;
+}
 // Inclusive prefix sum over the block's threads; their total in `total`.
 template <class T>
 __device__ __forceinline__ T block_scan(SampleShared& s, T v, T& total) {
-  const int w = threadIdx.x >> 6;
   v = wave_incl_scan(v);
-  if ((threadIdx.x & 63) == 63) s.red[w] = __builtin_bit_cast(uint64_t, v);
-  __syncthreads();
-  T add = 0, t = 0;
-#pragma unroll
-  for (int i = 0; i < kSamplePick / 64; ++i) {
-    const T x = __builtin_bit_cast(T, s.red[i]);
-    if (i < w) add += x;
-    t += x;
-  }
-  __syncthreads();
-  total = t;
-  return add + v;
+  const T t = waves_scan(s, v);
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  total = read_lane(t, 15);
+  return w ? read_lane(t, (w - 1) & 15) + v : v;
 }
 template <class T>
 __device__ __forceinline__ T block_total(SampleShared& s, T v) {
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) s.red[threadIdx.x >> 6] = __builtin_bit_cast(uint64_t, v);
-  __syncthreads();
-  T t = 0;
-#pragma unroll
-  for (int i = 0; i < kSamplePick / 64; ++i) t += __builtin_bit_cast(T, s.red[i]);
-  __syncthreads();
-  return t;
+  return read_lane(waves_scan(s, wave_sum(v)), 15);
 }
 
 // The first of n positions whose inclusive prefix reaches `target` > 0
@@ -306,15 +307,22 @@ __device__ __forceinline__ int block_find(SampleShared& s, int n, T target, F va
     T total;
     const T incl = base + block_scan(s, v, total);
     if (base + total >= target) {                  // uniform
-      // the lowest thread that reached it (rounding may make several doubles
-      // that did not grow look like the border: the lowest is taken)
-      if (threadIdx.x == 0) s.pos = 0x7fffffff;
-      __syncthreads();
-      if (incl >= target) atomicMin(&s.pos, i);
+      if constexpr (std::is_integral<T>::value) {
+        if (incl >= target && incl - v < target) { // exactly one thread
+          s.pos = i;
+          s.a = incl - v;
+        }
+      } else {
+        // rounding may leave several threads, or a position past n, that
+        // look like the border: the lowest is taken
+        if (threadIdx.x == 0) s.pos = 0x7fffffff;
+        __syncthreads();
+        if (incl >= target) atomicMin(&s.pos, i);
+        __syncthreads();
+        if (i == min(s.pos, n - 1)) s.a = __builtin_bit_cast(uint64_t, incl - v);
+      }
       __syncthreads();
       const int pos = min(s.pos, n - 1);
-      if (i == pos) s.a = __builtin_bit_cast(uint64_t, incl - v);
-      __syncthreads();
       before = __builtin_bit_cast(T, s.a);
       __syncthreads();
       return pos;
@@ -374,12 +382,12 @@ struct SamplePicker {
     return l == m ? 0 : (l == -INFINITY ? kSampleBins - 1 : b);
   }
   __device__ __forceinline__ uint64_t mass(float l) const {
-    return bin(l) < kSampleBins - 1 ? (uint64_t)rint(sample_weight(l, m, p.c64) * scale) : 0;
+    return (uint64_t)rint(sample_weight(l, m, p.c64) * scale);
   }
   // The mass if the id passes min_p, else 0.
   __device__ __forceinline__ uint64_t kept_mass(float l) const {
     const double w = sample_weight(l, m, p.c64);
-    return bin(l) < kSampleBins - 1 && w >= p.min_p ? (uint64_t)rint(w * scale) : 0;
+    return w >= p.min_p ? (uint64_t)rint(w * scale) : 0;
   }
   __device__ __forceinline__ bool passes_min_p(float l) const {
     return p.min_p == 0.0 || sample_weight(l, m, p.c64) >= p.min_p;
@@ -399,15 +407,27 @@ struct SamplePicker {
       A.logprob[r] = (float)((l == m ? 0.0 : ((double)l - (double)m) * p.c64 * (1.0 / 64.0)) - log((double)total / scale));
   }
 
+  // Calls f(group, its largest logit) for every group, each thread a strided
+  // share, four loads in flight.
+  template <class F>
+  __device__ __forceinline__ void for_groups(F f) const {
+    for (int i = threadIdx.x; i < A.groups; i += 4 * kSamplePick) {
+      float g[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = i + j * kSamplePick < A.groups ? gmax[i + j * kSamplePick] : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (g[j] > -INFINITY) f(i + j * kSamplePick, g[j]);
+    }
+  }
+
   // Lowest id of the largest logit.
   __device__ __forceinline__ void pick_greedy() {
     if (threadIdx.x == 0) s.pos = A.groups;
     __syncthreads();
-    for (int i = threadIdx.x; i < A.groups; i += kSamplePick)
-      if (gmax[i] == m) {
-        atomicMin(&s.pos, i);
-        break;
-      }
+    for_groups([&](int i, float g) {
+      if (g == m) atomicMin(&s.pos, i);
+    });
     __syncthreads();
     if (threadIdx.x < 64) {
       const int v = s.pos * kSampleGroup + (int)threadIdx.x;
@@ -426,7 +446,7 @@ struct SamplePicker {
     int* cnt = (int*)s.bins;
     for (int i = threadIdx.x; i < kSampleBins; i += kSamplePick) cnt[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < A.groups; i += kSamplePick) atomicAdd(&cnt[bin(gmax[i])], 1);
+    for_groups([&](int, float g) { atomicAdd(&cnt[bin(g)], 1); });
     __syncthreads();
     uint64_t before;
     // two bins per thread: one prefix sum covers them all
@@ -437,20 +457,21 @@ struct SamplePicker {
     return before + cnt[2 * b] >= (uint64_t)want ? 2 * b : 2 * b + 1;
   }
 
-  // All ids in bins <= b into s.key (unordered); their number, or a number
-  // past kSampleList if they do not fit.
-  __device__ __forceinline__ int gather(int b) {
+  // All ids in bins <= b into s.key (unordered), if their groups are at most
+  // `most`; their number, or one past kSampleList if they do not fit.
+  __device__ __forceinline__ int gather(int b, int most) {
     int* list = (int*)s.aux;                       // groups to read: 2 * kSampleList places
     if (threadIdx.x == 0) s.n = s.n2 = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < A.groups; i += kSamplePick)
-      if (bin(gmax[i]) <= b) {
+    for_groups([&](int i, float g) {
+      if (bin(g) <= b) {
         const int at = atomicAdd(&s.n2, 1);
         if (at < 2 * kSampleList) list[at] = i;
       }
+    });
     __syncthreads();
     const int ng = s.n2;
-    if (ng > kSampleList) return kSampleList + 1;  // at least one id each
+    if (ng > most) return kSampleList + 1;
     const int lane = threadIdx.x & 63;
     for (int g0 = (threadIdx.x >> 6) * 4; g0 < ng; g0 += 4 * (kSamplePick / 64)) {
       float x[4];
@@ -585,15 +606,19 @@ struct SamplePicker {
     return (int)fminf(b, (float)kSampleBins);      // -inf: outside
   }
 
-  // The kept set is every id in bins < lo and, in bins lo..hi, those with
-  // cand_key >= lim.
+  // The kept set: every id with l cb >= edge and, below it, those that are
+  // not after the id `last` with the logit `least` in descending order.
   struct Kept {
-    int lo, hi;
-    uint64_t lim;
+    float edge, least;
+    int last;
   };
+  // cand_key >= lim (0: all above -inf; ~0: none)
+  __device__ __forceinline__ static Kept kept_from(float edge, uint64_t lim) {
+    if (lim == 0) return Kept{edge, -INFINITY, -1};
+    return lim == ~0ull ? Kept{edge, INFINITY, -1} : Kept{edge, key_logit(lim), key_id(lim)};
+  }
   __device__ __forceinline__ bool is_kept(const Kept& k, int v, float l) const {
-    const int b = bin(l);
-    return v < A.V && b < kSampleBins - 1 && (b < k.lo || (b <= k.hi && cand_key(l, (uint32_t)v) >= k.lim));
+    return l * p.cb >= k.edge || l > k.least || (l == k.least && v <= k.last);
   }
 
   // Draw, given the segments' kept masses in s.bins.  A segment whose mass
@@ -617,8 +642,8 @@ struct SamplePicker {
     for (int j = 0; j < C / N; ++j) sample_load<E>(row, v0 + j * N, A.V, x + j * N);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      if (!is_kept(k, v0 + i, x[i])) x[i] = -INFINITY;
-      sum += kept_mass(x[i]);
+      sum += is_kept(k, v0 + i, x[i]) ? kept_mass(x[i]) : 0;
+      if (i & 1) asm volatile("" : "+v"(sum));     // two at a time: few registers
     }
     uint64_t all;
     uint64_t run = block_scan(s, sum, all) - sum;
@@ -630,17 +655,17 @@ struct SamplePicker {
     // (a segment's mass taken from its histogram may differ from this sum in
     // the last units: the target is held inside it)
     const uint64_t aim = min(want > before ? want - before : (uint64_t)1, all);
-    if (run < aim && run + sum >= aim) {           // one thread
-#pragma unroll 1
-      for (int i = 0; i < C; ++i) {
-        const float l = sample_logit(load_elem<E>(row + min(v0 + i, A.V - 1)));
-        const uint64_t w = v0 + i < A.V && is_kept(k, v0 + i, l) ? kept_mass(l) : 0;
-        run += w;
-        if (w && run >= aim) {
-          emit(v0 + i, l, total);
-          break;
-        }
-      }
+    if (run < aim && run + sum >= aim) {           // one thread; its ids to a wave
+      s.pos = v0;
+      s.a = run;
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      const int v = s.pos + (int)threadIdx.x;
+      const float l = (int)threadIdx.x < C && v < A.V ? sample_logit(load_elem<E>(row + v)) : -INFINITY;
+      const uint64_t w = is_kept(k, v, l) ? kept_mass(l) : 0;
+      const uint64_t incl = s.a + wave_incl_scan(w);
+      if (w && incl >= aim && incl - w < aim) emit(v, l, total);
     }
     return true;
   }
@@ -701,18 +726,70 @@ struct SamplePicker {
     const double above = block_total(s, part);     // (orders the writes above)
     const float lb = top - (float)hi, ub = top - (float)lo + 1.f;
     const float per = (float)kSampleSub / (float)(hi - lo + 1);
-    for_row([&](int v, float l) {
-      const float t = l * p.cb;
+    // 32 ids per thread and step: a bit each for those in the border, whose
+    // ids then go to the list (hardly any lane has more than two)
+    constexpr int D = 32 / N;
+    int* ids = (int*)s.key;
+    for (int v = (int)threadIdx.x * N; v < A.V; v += kSamplePick * 32) {
+      u32x4 u[D];
+#pragma unroll
+      for (int j = 0; j < D; ++j) {
+        const int vj = v + j * kSamplePick * N;
+        if (vj + N <= A.V) __builtin_memcpy(&u[j], row + vj, 16);
+        else u[j] = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};   // NaN of both types: in no bin
+      }
+      uint32_t hits = 0;
+#pragma unroll
+      for (int j = 0; j < D; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float l;
+          if constexpr (N == 8) l = __uint_as_float((i & 1) ? (u[j][i >> 1] & 0xffff0000u) : (u[j][i >> 1] << 16));
+          else l = __uint_as_float(u[j][i]);
+          const float t = l * p.cb;
+          hits |= t >= lb && t < ub ? 1u << (j * N + i) : 0u;
+        }
+      while (hits) {
+        const int q = __builtin_ctz(hits);
+        hits &= hits - 1;
+        const int at = atomicAdd(&s.n, 1);
+        if (at < kSampleList) ids[at] = v + (q / N) * (kSamplePick * N) + q % N;
+      }
+    }
+    // the last vector, where it crosses the row's end
+    if (threadIdx.x < A.V % N) {
+      const int v = A.V - A.V % N + (int)threadIdx.x;
+      const float t = load_elem<E>(row + v) * p.cb;
       if (t >= lb && t < ub) {
         const int at = atomicAdd(&s.n, 1);
-        if (at < kSampleList) s.key[at] = cand_key(l, (uint32_t)v);
-        if (p.top_p < 1.0) atomicAdd((unsigned long long*)&s.sub[min((int)((ub - t) * per), kSampleSub - 1)], (unsigned long long)mass(l));
+        if (at < kSampleList) ids[at] = v;
       }
-    });
+    }
     __syncthreads();
     const int n = s.n;
     __syncthreads();
     if (n > kSampleList) return false;
+    // ids to keys, and the mass of each part of the border
+    constexpr int P = kSampleList / kSamplePick;
+    uint64_t key[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int i = (int)threadIdx.x + j * kSamplePick;
+      key[j] = 0;
+      if (i < n) key[j] = cand_key(sample_logit(load_elem<E>(row + ids[i])), (uint32_t)ids[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int i = (int)threadIdx.x + j * kSamplePick;
+      if (i >= n) continue;
+      s.key[i] = key[j];
+      if (p.top_p < 1.0) {
+        const float l = key_logit(key[j]);
+        atomicAdd((unsigned long long*)&s.sub[min((int)((ub - l * p.cb) * per), kSampleSub - 1)], (unsigned long long)mass(l));
+      }
+    }
+    __syncthreads();
     // which of them stay: those that pass min_p and, with top_p, the whole
     // sub-bins above the one where their mass reaches its share, and of that
     // one's ids, sorted, the first
@@ -739,7 +816,7 @@ struct SamplePicker {
         }
       }
     }
-    k = Kept{lo, hi, lim};
+    k = kept_from(ub, lim);
     // the segments' masses above the border, a wave per segment, then the
     // border's kept ids
     double* fac = (double*)s.aux;
@@ -848,7 +925,7 @@ struct SamplePicker {
     if (p.top_k > 0) lim = cut<false>(lim, [&](uint64_t) { return (uint64_t)p.top_k; });
     if (p.top_p < 1.0)
       lim = cut<true>(lim, [&](uint64_t total) { return (uint64_t)fmax(ceil(p.top_p * (double)total), 1.0); });
-    const Kept k{0, kSampleBins - 1, lim};
+    const Kept k = kept_from(INFINITY, lim);
     for (int i = threadIdx.x; i < A.segs; i += kSamplePick) s.bins[i] = 0;
     __syncthreads();
     // a wave's ids of one vector lie in one segment (64 * N divides it)
@@ -887,7 +964,7 @@ struct SamplePicker {
     if (p.greedy) return pick_greedy();
     set_max(m);
     const int mode = sample_scan_mode(A, p);
-    Kept k{0, kSampleBins - 1, 0};
+    Kept k = kept_from(INFINITY, 0);
     if (mode == kScanMass) {
       for (int i = threadIdx.x; i < A.segs; i += kSamplePick) {
         const double v = A.smass[(int64_t)r * A.segs + i];
@@ -905,8 +982,10 @@ struct SamplePicker {
       // (top_p of top_k's ids needs the mass of all of them)
       if (!hist && p.min_p > 0.0 && p.top_p == 1.0)
         hi = min(hi, (int)fmin(-64.0 * log(p.min_p) + 3.0, (double)(kSampleBins - 2)));
-      const int n = gather(hi);
-      if (n <= kSampleList) {
+      // (a histogram's row takes the list only if it can be ranked at once:
+      // longer lists cost more than the border's ids alone)
+      const int n = gather(hi, hist ? kSampleRank : kSampleList);
+      if (n <= (hist ? kSampleRank : kSampleList)) {
         if (!hist && p.top_k == 0 && p.top_p < 1.0) {
           uint64_t part = 0;
           for (int i = threadIdx.x; i < n; i += kSamplePick) part += mass(key_logit(s.key[i]));
