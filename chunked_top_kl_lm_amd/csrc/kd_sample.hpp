@@ -9,7 +9,7 @@
 //
 // Borders between ids are decided in 64 bits: w is a double from a polynomial
 // (relative error about 1e-14), and masses that ids are picked by are sums of
-// 64-bit integers, W_v = rint(w_v 2^s) with s = 62 - ceil(log2 V), at most 52:
+// 64-bit integers, W_v = rint(w_v 2^s) with s = 62 - ceil(log2 V), at most 51:
 // integer sums do not depend on their order, so LDS atomics keep the result
 // the same from call to call.  An id more than about 32 T below the largest
 // logit (w < 1.3e-14) has W = 0.  NaN and -inf logits have no mass; a +inf
@@ -106,7 +106,7 @@ __device__ __forceinline__ int sample_scan_mode(const SampleArgs& A, const Sampl
 }
 
 // A logit as the operator sees it: NaN as -inf, -0 as +0.
-__device__ __forceinline__ float sample_logit(float x) { return x == x ? x + 0.f : -INFINITY; }
+__device__ __forceinline__ float sample_logit(float x) { return fmaxf(x + 0.f, -INFINITY); }
 
 // exp((l - m) c64 / 64).  2^f on |f| <= 1/2 by the Taylor series of exp in
 // f ln 2 up to degree 12 (remainder 0.3466^13 / 13! < 2e-16).
@@ -132,22 +132,40 @@ __device__ __forceinline__ double sample_weight(float l, float m, double c64) {
   const double w = __longlong_as_double(__double_as_longlong(p) + (long long)(int)k * (1ll << 52));
   return l == m ? 1.0 : (y0 > -64.0 ? w : 0.0);
 }
-// exp(y / 64) for |y| <= 1.5 (a logit against its bin's edge): degree 6,
-// remainder 0.0235^7 / 7! < 1e-15.
-__device__ __forceinline__ double edge_weight(double y) {
-  const double x = y * (1.0 / 64.0);
-  double p = 1.0 / 720.0;
-  p = fma(p, x, 1.0 / 120.0);
-  p = fma(p, x, 1.0 / 24.0);
-  p = fma(p, x, 1.0 / 6.0);
-  p = fma(p, x, 0.5);
-  p = fma(p, x, 1.0);
-  return fma(p, x, 1.0);
-}
+// exp(y / 64) for |y| <= 1.5 (a logit against its bin's edge): degree 6 in
+// y / 64, remainder 0.0235^7 / 7! < 1e-15.  The coefficients are held in
+// scalar registers, so that a step of the polynomial is one instruction.
+struct EdgeWeight {
+  double c[6];
+  __device__ __forceinline__ EdgeWeight() {
+    constexpr double h = 1.0 / 64.0;
+    c[0] = h;
+    c[1] = h * h / 2.0;
+    c[2] = h * h * h / 6.0;
+    c[3] = h * h * h * h / 24.0;
+    c[4] = h * h * h * h * h / 120.0;
+    c[5] = h * h * h * h * h * h / 720.0;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) asm("" : "+s"(c[i]));
+  }
+  __device__ __forceinline__ double operator()(double y) const {
+    double p = fma(c[5], y, c[4]);
+    p = fma(p, y, c[3]);
+    p = fma(p, y, c[2]);
+    p = fma(p, y, c[1]);
+    p = fma(p, y, c[0]);
+    return fma(p, y, 1.0);
+  }
+};
 // Units of the masses, 2^s.
 __device__ __forceinline__ double sample_scale(int V) {
   const int bits = 62 - (32 - __clz(max(V - 1, 1)));
-  return (double)(1ull << min(bits, 52));
+  return (double)(1ull << min(bits, 51));
+}
+// rint(w * scale) for products below 2^52: added to 2^52 the integer is the
+// low bits of the sum.
+__device__ __forceinline__ uint64_t sample_units(double w, double scale) {
+  return (uint64_t)__double_as_longlong(fma(w, scale, 4503599627370496.0)) - 0x4330000000000000ull;
 }
 
 // 16 bytes of consecutive logits of a row (-inf past its end).
@@ -232,17 +250,27 @@ __global__ __launch_bounds__(kSampleScan) void sample_scan_kernel(SampleArgs A) 
     int last = -1;
     if (fabsf(top) < kSampleGrid) {                // false for -inf and NaN
       const double scale = sample_scale(A.V);
+      const EdgeWeight weight;
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float b = floorf(x[j][i] * p.cb);
-          const float d = top - b;
-          if (d < (float)(kSampleBins - 1)) {      // false for -inf
-            const double w = edge_weight(fma((double)x[j][i], p.c64, -((double)b + 1.0)));
-            atomicAdd(&s_hist[(int)d], (unsigned long long)rint(w * scale));
-            last = max(last, (int)d);
+        for (int q = 0; q < N; q += 4) {
+          // four ids at a time: their polynomials interleave
+          float d[4];
+          uint64_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float b = floorf(x[j][q + i] * p.cb);
+            d[i] = top - b;
+            w[i] = sample_units(weight(fma((double)x[j][q + i], p.c64, -(double)(b + 1.f))), scale);
+            asm volatile("" : "+v"(w[i]), "+v"(d[i]));
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (d[i] < (float)(kSampleBins - 1)) { // false for -inf
+              atomicAdd(&s_hist[(int)d[i]], (unsigned long long)w[i]);
+              last = max(last, (int)d[i]);
+            }
         }
     }
     if (last >= 0) atomicMax(&s_len, last + 1);
@@ -382,12 +410,12 @@ struct SamplePicker {
     return l == m ? 0 : (l == -INFINITY ? kSampleBins - 1 : b);
   }
   __device__ __forceinline__ uint64_t mass(float l) const {
-    return (uint64_t)rint(sample_weight(l, m, p.c64) * scale);
+    return sample_units(sample_weight(l, m, p.c64), scale);
   }
   // The mass if the id passes min_p, else 0.
   __device__ __forceinline__ uint64_t kept_mass(float l) const {
     const double w = sample_weight(l, m, p.c64);
-    return w >= p.min_p ? (uint64_t)rint(w * scale) : 0;
+    return w >= p.min_p ? sample_units(w, scale) : 0;
   }
   __device__ __forceinline__ bool passes_min_p(float l) const {
     return p.min_p == 0.0 || sample_weight(l, m, p.c64) >= p.min_p;
@@ -679,18 +707,19 @@ struct SamplePicker {
     int2* seg = (int2*)s.aux;
     for (int sg = threadIdx.x; sg < A.segs; sg += kSamplePick) seg[sg] = make_int2(seg_offset(sg), A.hlen[at0 + sg]);
     __syncthreads();
-    double part = 0.0;
-    for (int j = threadIdx.x; j < kSampleBins; j += kSamplePick) {
-      uint64_t a = 0;
+    static_assert(kSampleBins == 2 * kSamplePick, "two bins per thread");
+    const int j0 = threadIdx.x, j1 = j0 + kSamplePick;
+    uint64_t a0 = 0, a1 = 0;
 #pragma unroll 8
-      for (int sg = 0; sg < A.segs; ++sg) {
-        const int i = j - seg[sg].x;
-        a += i >= 0 && i < seg[sg].y ? A.hist[(at0 + sg) * kSampleBins + i] : 0;
-      }
-      const double v = a && j < kSampleBins - 1 ? (double)a * bin_factor(j) : 0.0;
-      bm[j] = v;
-      part += v;
+    for (int sg = 0; sg < A.segs; ++sg) {
+      const int2 at = seg[sg];
+      const uint64_t* h = A.hist + (at0 + sg) * kSampleBins - at.x;
+      a0 += j0 >= at.x && j0 - at.x < at.y ? h[j0] : 0;
+      a1 += j1 >= at.x && j1 - at.x < at.y ? h[j1] : 0;
     }
+    bm[j0] = a0 ? (double)a0 * bin_factor(j0) : 0.0;
+    bm[j1] = a1 && j1 < kSampleBins - 1 ? (double)a1 * bin_factor(j1) : 0.0;
+    const double part = bm[j0] + bm[j1];
     const double all = block_total(s, part);       // (orders the writes)
     const double need = p.top_p * all;
     lo = kSampleBins - 1;
