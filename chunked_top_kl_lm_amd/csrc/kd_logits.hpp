@@ -5,13 +5,12 @@
 // epilogue that writes row t's logits along v.  Bound by the matrix cores.
 //
 // Few rows (a decoding step): every element of W is used T times only, so the
-// product is bound by reading W once.  skinny_logits_kernel needs no LDS and
-// no barrier: a wave owns 16 vocabulary rows, streams them straight from HBM
-// into matrix-core operands (v_mfma_f32_16x16x32_bf16: lane l supplies row
-// l % 16 and eight consecutive k; fp32: four v_mfma_f32_16x16x4_f32 per
-// 16-byte unit) and multiplies each by up to 16 * NT hidden rows, which
-// stay in the caches.  Several K steps of loads are issued ahead of their
-// products, and thousands of waves keep HBM busy.
+// product is bound by reading W once.  In skinny_logits_kernel a wave owns 16
+// vocabulary rows and streams them from HBM straight into matrix-core operands
+// (v_mfma_f32_16x16x32_bf16: lane l supplies row l % 16 and eight consecutive
+// k; fp32: four v_mfma_f32_16x16x4_f32 per 16-byte unit), a chunk of 512 bytes
+// per row ahead of the products.  The hidden rows' chunk, which all waves need,
+// goes through LDS once per block (two buffers, one barrier per chunk).
 #pragma once
 
 #include "kd_gemm.hpp"
@@ -104,7 +103,9 @@ template <> __device__ __forceinline__ void mfma16_unit<F32>(f32x4& acc, u32x4 a
 }
 
 constexpr int kSkinnyWaves = 4;    // waves (16 vocabulary rows each) per block
-constexpr int kSkinnyAhead = 8;    // K steps of W in flight per wave
+constexpr int kSkinnySteps = 8;    // K steps (64 bytes of a row) per chunk
+constexpr int kSkinnyRow = 64 * kSkinnySteps + 16;   // LDS bytes of a hidden row's chunk: a fragment's 16 rows
+                                                     // start 4 banks apart and cover all 64
 
 // z for up to 16 * NT rows.  Accumulator layout of the 16x16 tiles: register
 // r of lane l holds C[4 * (l / 16) + r][l % 16]: four consecutive v of one row t.
@@ -112,40 +113,78 @@ template <class E, int NT>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_logits_kernel(const typename E::T* H, int64_t ldh, int T,
                                                                           const typename E::T* W, int V, int d,
                                                                           float* z, int64_t ldz) {
-  constexpr int kUnit = 16 / E::kBytes;             // elements per lane and K step
-  constexpr int kStep = 4 * kUnit;                  // elements of K per step
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kUnit = 16 / E::kBytes;             // elements of a 16-byte unit
+  constexpr int kStep = 4 * kUnit;                  // of a K step
+  constexpr int kChunk = kSkinnySteps * kStep;
+  constexpr int kUnits = 4 * kSkinnySteps;          // units of a row's chunk
+  constexpr int kStage = 16 * NT * kUnits / (64 * kSkinnyWaves);   // units staged per thread
+  __shared__ __attribute__((aligned(16))) char s_h[2][16 * NT * kSkinnyRow];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int v0 = (blockIdx.x * kSkinnyWaves + wave) * 16;
-  if (v0 >= V) return;
-  const int row = lane & 15, kl = (lane >> 4) * kUnit;
+  const int row = lane & 15, ul = lane >> 4;        // fragment row, unit of a step
   const typename E::T* w = W + (int64_t)min(v0 + row, V - 1) * d;
-  const typename E::T* h[NT];
-  int dh[NT];                                       // rows past T read nothing: zeros
+  const int chunks = (d + kChunk - 1) / kChunk;
+
+  u32x4 hs[kStage];
+  auto load_h = [&](int c) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int t = 16 * n + row;
-    h[n] = H + (int64_t)min(t, T - 1) * ldh;
-    dh[n] = t < T ? d : 0;
-  }
+    for (int i = 0; i < kStage; ++i) {
+      const int q = tid + i * 64 * kSkinnyWaves, t = q / kUnits, u = q % kUnits;
+      hs[i] = unit16<E>(H + (int64_t)min(t, T - 1) * ldh, c * kChunk + u * kUnit, t < T ? d : 0);   // t >= T: zeros
+    }
+  };
+  auto store_h = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+      const int q = tid + i * 64 * kSkinnyWaves, t = q / kUnits, u = q % kUnits;
+      *(u32x4*)(s_h[c & 1] + t * kSkinnyRow + u * 16) = hs[i];
+    }
+  };
+  auto load_w = [&](u32x4 (&a)[kSkinnySteps], int c) {
+    if ((c + 1) * kChunk <= d) {                    // uniform
+#pragma unroll
+      for (int i = 0; i < kSkinnySteps; ++i) __builtin_memcpy(&a[i], w + c * kChunk + i * kStep + ul * kUnit, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSkinnySteps; ++i) a[i] = unit16<E>(w, c * kChunk + i * kStep + ul * kUnit, d);
+    }
+  };
   f32x4 acc[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int k = 0;
-  for (; k + kSkinnyAhead * kStep <= d; k += kSkinnyAhead * kStep) {
-    u32x4 a[kSkinnyAhead];
+  auto multiply = [&](const u32x4 (&a)[kSkinnySteps], int c) {
+    const char* h = s_h[c & 1] + row * kSkinnyRow + ul * 16;
 #pragma unroll
-    for (int i = 0; i < kSkinnyAhead; ++i) __builtin_memcpy(&a[i], w + k + i * kStep + kl, 16);
+    for (int i = 0; i < kSkinnySteps; ++i)
 #pragma unroll
-    for (int i = 0; i < kSkinnyAhead; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mfma16_unit<E>(acc[n], a[i], unit16<E>(h[n], k + i * kStep + kl, dh[n]));
+      for (int n = 0; n < NT; ++n) mfma16_unit<E>(acc[n], a[i], *(const u32x4*)(h + 16 * n * kSkinnyRow + 64 * i));
+  };
+
+  u32x4 a0[kSkinnySteps], a1[kSkinnySteps];
+  load_w(a0, 0);
+  load_h(0);
+  store_h(0);
+  __syncthreads();
+  // the next chunk's loads are in flight while this one is multiplied; a
+  // buffer is rewritten after the barrier that follows its last reads
+  for (int c = 0; c < chunks; c += 2) {
+    if (c + 1 < chunks) {
+      load_w(a1, c + 1);
+      load_h(c + 1);
+    }
+    multiply(a0, c);
+    if (c + 1 >= chunks) break;
+    store_h(c + 1);
+    __syncthreads();
+    if (c + 2 < chunks) {
+      load_w(a0, c + 2);
+      load_h(c + 2);
+    }
+    multiply(a1, c + 1);
+    if (c + 2 < chunks) store_h(c + 2);
+    __syncthreads();
   }
-  for (; k < d; k += kStep) {
-    const u32x4 a = unit16<E>(w, k + kl, d);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) mfma16_unit<E>(acc[n], a, unit16<E>(h[n], k + kl, dh[n]));
-  }
-  const int v = v0 + 4 * (lane >> 4);
+  const int v = v0 + 4 * ul;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int t = 16 * n + row;
