@@ -76,13 +76,14 @@ int32_t logits_run(const LogitsPlan& P, const void* hidden, int64_t ldh, const v
                    int64_t V, float* logits, char* ws, hipStream_t st) {
   typedef typename E::T S;
   if (P.skinny) {
-    const dim3 grid((unsigned)cdiv(V, 16 * kSkinnyWaves));
+    const dim3 grid((unsigned)cdiv(V, 16 * kSkinnyWaves)), block(64 * kSkinnyWaves);
+    const S *h = (const S*)hidden, *w = (const S*)W;
     if (T <= 16)
-      hipLaunchKernelGGL((skinny_logits_kernel<E, 1>), grid, dim3(64 * kSkinnyWaves), 0, st, (const S*)hidden, ldh,
-                         (int)T, (const S*)W, (int)V, (int)d, logits, V);
+      hipLaunchKernelGGL((skinny_logits_kernel<E, 1>), grid, block, 0, st, h, ldh, (int)T, w, (int)V, (int)d, logits, V);
+    else if (T <= 32)
+      hipLaunchKernelGGL((skinny_logits_kernel<E, 2>), grid, block, 0, st, h, ldh, (int)T, w, (int)V, (int)d, logits, V);
     else
-      hipLaunchKernelGGL((skinny_logits_kernel<E, 2>), grid, dim3(64 * kSkinnyWaves), 0, st, (const S*)hidden, ldh,
-                         (int)T, (const S*)W, (int)V, (int)d, logits, V);
+      hipLaunchKernelGGL((skinny_logits_kernel<E, 4>), grid, block, 0, st, h, ldh, (int)T, w, (int)V, (int)d, logits, V);
     KD_LAUNCH_CHECK();
     return KD_OK;
   }
@@ -109,8 +110,11 @@ int32_t logits_run(const LogitsPlan& P, const void* hidden, int64_t ldh, const v
       ld = P.d_p;
     }
     const EpiStoreLogits epi{logits + t0 * V, V, (int)V, (int)n};
-    const GemmShape g = make_shape<TileMain>(w, ldw, (int)V, h, ld, (int)n, P.d_p * E::kBytes, 1, 1);
-    if (launch_gemm<TileMain, E>(g, epi, st) != hipSuccess) return KD_ERR_HIP;
+    const int64_t kbytes = P.d_p * E::kBytes;
+    const hipError_t e =
+        P.tall ? launch_gemm<TileLogits, E>(make_shape<TileLogits>(w, ldw, (int)V, h, ld, (int)n, kbytes, 1, 1), epi, st)
+               : launch_gemm<TileMain, E>(make_shape<TileMain>(w, ldw, (int)V, h, ld, (int)n, kbytes, 1, 1), epi, st);
+    if (e != hipSuccess) return KD_ERR_HIP;
   }
   return KD_OK;
 }

@@ -8,7 +8,7 @@
 // product is bound by reading W once.  In skinny_logits_kernel a wave owns 16
 // vocabulary rows and streams them from HBM straight into matrix-core operands
 // (v_mfma_f32_16x16x32_bf16: lane l supplies row l % 16 and eight consecutive
-// k; fp32: four v_mfma_f32_16x16x4_f32 per 16-byte unit), a chunk of 512 bytes
+// k; fp32: four v_mfma_f32_16x16x4_f32 per 16-byte unit), a chunk of 256 bytes
 // per row ahead of the products.  The hidden rows' chunk, which all waves need,
 // goes through LDS once per block (two buffers, one barrier per chunk).
 #pragma once
@@ -18,11 +18,12 @@
 
 namespace kd {
 
-// GEMM epilogue: columns 32 j .. + 31 of the wave's tile are staged in its
-// share of the freed LDS ring as [32 t][32 FM v] fp32 (16-byte unit u of row
-// t at u ^ (t mod units): conflict-free writes and reads) and leave as
-// 16-byte stores of whole row segments.  Rows of z start at any multiple of
-// 4 bytes; units that cross the end of a row are stored element by element.
+// GEMM epilogue: columns 32 j .. + 31 of the wave's tile, up to four 32-row
+// tiles at a time, are staged in its share of the freed LDS ring as [32 t][32 B
+// v] fp32 (16-byte unit u of row t at u ^ (t mod units): conflict-free writes
+// and reads) and leave as 16-byte stores of whole row segments.  Rows of z
+// start at any multiple of 4 bytes; units that cross the end of a row are
+// stored element by element.
 struct EpiStoreLogits {
   float* z;       // [N][M]
   int64_t ldz;
@@ -30,44 +31,55 @@ struct EpiStoreLogits {
 
   template <int FM, int FN>
   __device__ __forceinline__ void apply(f32x16 (&acc)[FM][FN], const EpiCtx& c) const {
-    if (c.m0 >= M) return;
-    constexpr int U = 8 * FM;                       // 16-byte units per staged row
-    constexpr int RPI = 64 / U;                     // rows per read of the wave
-    char* lds = c.smem + c.wid * (c.smem_bytes / c.nwaves);
-    const int tl = acc_col(c.lane);
+    static_assert(FM <= 5, "one group of four tiles and one more");
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       if (c.n0 + 32 * j >= N) break;
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int g4 = 0; g4 < 4; ++g4) {
-          const int u = 8 * i + 2 * g4 + (c.lane >> 5);
-          *(f32x4*)(lds + tl * (U * 16) + ((u ^ (tl & (U - 1))) << 4)) =
-              f32x4{acc[i][j][4 * g4], acc[i][j][4 * g4 + 1], acc[i][j][4 * g4 + 2], acc[i][j][4 * g4 + 3]};
-        }
-      __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0): the wave's staging writes are done
-      const int u = c.lane & (U - 1);
-      const int v = c.m0 + 4 * u;
-#pragma unroll
-      for (int q = 0; q < 32 / RPI; ++q) {
-        const int r = q * RPI + c.lane / U;
-        const f32x4 val = *(const f32x4*)(lds + r * (U * 16) + ((u ^ (r & (U - 1))) << 4));
-        const int t = c.n0 + 32 * j + r;
-        if (t >= N) continue;
-        float* o = z + (int64_t)t * ldz + v;
-        if (v + 4 <= M) {
-          __builtin_memcpy(o, &val, 16);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (v + e < M) o[e] = val[e];
-        }
-      }
-      // the wave's LDS operations run in order: the next half's writes
-      // follow this half's reads
-      __builtin_amdgcn_s_waitcnt(0xC07F);
+      constexpr int B = FM < 4 ? FM : 4;
+      store<B, 0>(acc, j, c);
+      if constexpr (FM == 5) store<1, 4>(acc, j, c);
     }
+  }
+
+  // tiles I0 .. I0 + B - 1 of the wave's rows
+  template <int B, int I0, int FM, int FN>
+  __device__ __forceinline__ void store(f32x16 (&acc)[FM][FN], int j, const EpiCtx& c) const {
+    static_assert(B == 1 || B == 2 || B == 4, "units per staged row");
+    constexpr int U = 8 * B;                        // 16-byte units per staged row
+    constexpr int RPI = 64 / U;                     // rows per read of the wave
+    if (c.m0 + 32 * I0 >= M) return;
+    char* lds = c.smem + c.wid * (c.smem_bytes / c.nwaves);
+    const int tl = acc_col(c.lane);
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int g4 = 0; g4 < 4; ++g4) {
+        const int u = 8 * i + 2 * g4 + (c.lane >> 5);
+        const f32x16& a = acc[I0 + i][j];
+        *(f32x4*)(lds + tl * (U * 16) + ((u ^ (tl & (U - 1))) << 4)) =
+            f32x4{a[4 * g4], a[4 * g4 + 1], a[4 * g4 + 2], a[4 * g4 + 3]};
+      }
+    __builtin_amdgcn_s_waitcnt(0xC07F);             // lgkmcnt(0): the wave's staging writes are done
+    const int u = c.lane & (U - 1);
+    const int v = c.m0 + 32 * I0 + 4 * u;
+#pragma unroll
+    for (int q = 0; q < 32 / RPI; ++q) {
+      const int r = q * RPI + c.lane / U;
+      const f32x4 val = *(const f32x4*)(lds + r * (U * 16) + ((u ^ (r & (U - 1))) << 4));
+      const int t = c.n0 + 32 * j + r;
+      if (t >= N) continue;
+      float* o = z + (int64_t)t * ldz + v;
+      if (v + 4 <= M) {
+        __builtin_memcpy(o, &val, 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (v + e < M) o[e] = val[e];
+      }
+    }
+    // the wave's LDS operations run in order: the next group's writes follow
+    // this group's reads
+    __builtin_amdgcn_s_waitcnt(0xC07F);
   }
 };
 
@@ -103,7 +115,7 @@ template <> __device__ __forceinline__ void mfma16_unit<F32>(f32x4& acc, u32x4 a
 }
 
 constexpr int kSkinnyWaves = 4;    // waves (16 vocabulary rows each) per block
-constexpr int kSkinnySteps = 8;    // K steps (64 bytes of a row) per chunk
+constexpr int kSkinnySteps = 4;    // K steps (64 bytes of a row) per chunk
 constexpr int kSkinnyRow = 64 * kSkinnySteps + 16;   // LDS bytes of a hidden row's chunk: a fragment's 16 rows
                                                      // start 4 banks apart and cover all 64
 

@@ -37,6 +37,7 @@ using TileMain = TileCfg<256, 256, 2, 4, 2, 128>;
 using TileDhWide = TileCfg<256, 320, 4, 2, 2, 128>;
 using TileHead = TileCfg<256, 192, 4, 2, 2, 128>;
 using TileHeadNarrow = TileCfg<256, 128, 4, 2, 2, 128>;
+using TileLogits = TileCfg<320, 256, 2, 4, 2, 128>;      // 8 waves of 160 x 64
 constexpr int kBM = TileMain::BM, kBN = TileMain::BN;
 constexpr int kWaveM = TileMain::BM / TileMain::WM;   // vocabulary strip of one LSE partial
 constexpr int kNumCU = 256;           // MI355X compute units (split-K sizing)
@@ -249,10 +250,11 @@ inline size_t norm_bwd_workspace(int64_t T, int64_t d) {
 
 // Head logits: rows up to kSkinnyRows take the product that reads W once;
 // more run on the GEMM, kLogitRows at a time.
-constexpr int64_t kSkinnyRows = 32;
+constexpr int64_t kSkinnyRows = 64;
 constexpr int64_t kLogitRows = 8192;
 struct LogitsPlan {
   bool skinny, pad_w, pad_h;
+  bool tall;          // 320-row tiles
   int64_t d_p, rows;
   size_t off_wp, off_hp, total;
 };
@@ -266,6 +268,10 @@ inline int32_t make_logits_plan(int64_t T, int64_t d, int64_t V, int32_t dt, boo
   p->skinny = T <= kSkinnyRows;
   p->d_p = round_up(d, 64);
   p->rows = std::min<int64_t>(T, kLogitRows);
+  // one block per CU: the time goes by whole rounds of kNumCU tiles
+  const int64_t cols = cdiv(p->rows, TileMain::BN);
+  auto rounds = [&](int64_t bm) { return cdiv(cdiv(V, bm) * cols, kNumCU) * bm; };
+  p->tall = rounds(TileLogits::BM) < rounds(TileMain::BM);
   p->pad_w = !p->skinny && (d % 64 != 0 || !aligned_w);
   p->pad_h = !p->skinny && (d % 64 != 0 || !aligned_h);
   size_t o = 0;
