@@ -76,14 +76,17 @@ int32_t logits_run(const LogitsPlan& P, const void* hidden, int64_t ldh, const v
                    int64_t V, float* logits, char* ws, hipStream_t st) {
   typedef typename E::T S;
   if (P.skinny) {
-    const dim3 grid((unsigned)cdiv(V, 16 * kSkinnyWaves)), block(64 * kSkinnyWaves);
     const S *h = (const S*)hidden, *w = (const S*)W;
-    if (T <= 16)
-      hipLaunchKernelGGL((skinny_logits_kernel<E, 1>), grid, block, 0, st, h, ldh, (int)T, w, (int)V, (int)d, logits, V);
-    else if (T <= 32)
-      hipLaunchKernelGGL((skinny_logits_kernel<E, 2>), grid, block, 0, st, h, ldh, (int)T, w, (int)V, (int)d, logits, V);
-    else
-      hipLaunchKernelGGL((skinny_logits_kernel<E, 4>), grid, block, 0, st, h, ldh, (int)T, w, (int)V, (int)d, logits, V);
+    auto launch = [&](auto kernel, int waves) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(V, 16 * waves)), dim3(64 * waves), 0, st, h, ldh, (int)T, w,
+                         (int)V, (int)d, logits, V);
+    };
+    // more waves share a block's hidden rows as these grow: at d = 2880, V =
+    // 201088, 32 rows take 234 us with eight waves and 245 with four, 64 rows
+    // 278 and 284; one row 204 with four and 212 with eight
+    if (T <= 16) launch(skinny_logits_kernel<E, 1, 4>, 4);
+    else if (T <= 32) launch(skinny_logits_kernel<E, 2, 8>, 8);
+    else launch(skinny_logits_kernel<E, 4, 8>, 8);
     KD_LAUNCH_CHECK();
     return KD_OK;
   }

@@ -114,25 +114,24 @@ template <> __device__ __forceinline__ void mfma16_unit<F32>(f32x4& acc, u32x4 a
   acc = __builtin_amdgcn_mfma_f32_16x16x4f32(fa.w, fb.w, acc, 0, 0, 0);
 }
 
-constexpr int kSkinnyWaves = 4;    // waves (16 vocabulary rows each) per block
 constexpr int kSkinnySteps = 4;    // K steps (64 bytes of a row) per chunk
 constexpr int kSkinnyRow = 64 * kSkinnySteps + 16;   // LDS bytes of a hidden row's chunk: a fragment's 16 rows
                                                      // start 4 banks apart and cover all 64
 
 // z for up to 16 * NT rows.  Accumulator layout of the 16x16 tiles: register
 // r of lane l holds C[4 * (l / 16) + r][l % 16]: four consecutive v of one row t.
-template <class E, int NT>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_logits_kernel(const typename E::T* H, int64_t ldh, int T,
+template <class E, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void skinny_logits_kernel(const typename E::T* H, int64_t ldh, int T,
                                                                           const typename E::T* W, int V, int d,
                                                                           float* z, int64_t ldz) {
   constexpr int kUnit = 16 / E::kBytes;             // elements of a 16-byte unit
   constexpr int kStep = 4 * kUnit;                  // of a K step
   constexpr int kChunk = kSkinnySteps * kStep;
   constexpr int kUnits = 4 * kSkinnySteps;          // units of a row's chunk
-  constexpr int kStage = 16 * NT * kUnits / (64 * kSkinnyWaves);   // units staged per thread
+  constexpr int kStage = 16 * NT * kUnits / (64 * WAVES);   // units staged per thread
   __shared__ __attribute__((aligned(16))) char s_h[2][16 * NT * kSkinnyRow];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int v0 = (blockIdx.x * kSkinnyWaves + wave) * 16;
+  const int v0 = (blockIdx.x * WAVES + wave) * 16;
   const int row = lane & 15, ul = lane >> 4;        // fragment row, unit of a step
   const typename E::T* w = W + (int64_t)min(v0 + row, V - 1) * d;
   const int chunks = (d + kChunk - 1) / kChunk;
@@ -141,14 +140,14 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_logits_kernel(const 
   auto load_h = [&](int c) {
 #pragma unroll
     for (int i = 0; i < kStage; ++i) {
-      const int q = tid + i * 64 * kSkinnyWaves, t = q / kUnits, u = q % kUnits;
+      const int q = tid + i * 64 * WAVES, t = q / kUnits, u = q % kUnits;
       hs[i] = unit16<E>(H + (int64_t)min(t, T - 1) * ldh, c * kChunk + u * kUnit, t < T ? d : 0);   // t >= T: zeros
     }
   };
   auto store_h = [&](int c) {
 #pragma unroll
     for (int i = 0; i < kStage; ++i) {
-      const int q = tid + i * 64 * kSkinnyWaves, t = q / kUnits, u = q % kUnits;
+      const int q = tid + i * 64 * WAVES, t = q / kUnits, u = q % kUnits;
       *(u32x4*)(s_h[c & 1] + t * kSkinnyRow + u * 16) = hs[i];
     }
   };

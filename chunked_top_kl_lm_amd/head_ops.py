@@ -50,6 +50,15 @@ def declare(L) -> None:
         getattr(L, name).restype = i32
 
 
+def _stream(dev):
+    """Handle of the current stream of `dev`.  Small calls are bound by the
+    host; where torch has it, the handle without a Stream object around it is
+    taken (0.1 instead of 1.9 us)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _call(dev, name, *args):
     """Enqueue one entry point on the current stream of `dev` (its last
     argument), with that device current."""
@@ -57,10 +66,10 @@ def _call(dev, name, *args):
     kd = _pkg()
     fn = getattr(kd.lib(), name)
     if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        rc = fn(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, _stream(dev))
     if rc != 0:
         raise kd.KdError(rc)
 
@@ -191,9 +200,9 @@ def layer_norm_fwd(x, weight, bias=None, eps: float = 1e-5, checkpoint=None):
     T, d, ld = _rows("x", x)
     wdt = _check_weight(dev, d, dt, weight, bias)
     _check_kind(checkpoint)
-    y = torch.empty((T, d), dtype=x.dtype, device=dev)
+    y = torch.empty((T, d), dtype=x.dtype, device=dev) if ld != d else torch.empty_like(x)
     mean = torch.empty(T, dtype=torch.float32, device=dev)
-    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
     q = scale = None
     if checkpoint is not None:
         q = torch.empty((T, d), dtype=torch.int8, device=dev)
@@ -232,9 +241,9 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, need_dx: bool = True, need_dweight
     kd._check_device(dev, mean=mean, rstd=rstd)
     _expect("mean", mean, torch.float32, (T,))
     _expect("rstd", rstd, torch.float32, (T,))
-    dx = torch.empty((T, d), dtype=dy.dtype, device=dev) if need_dx else None
+    dx = torch.empty_like(dy) if need_dx else None
     dw = torch.empty(d, dtype=torch.float32, device=dev) if need_dweight else None
-    db = torch.empty(d, dtype=torch.float32, device=dev) if need_dweight else None
+    db = torch.empty_like(dw) if need_dweight else None
     ws = None
     if need_dweight:
         ws = _workspace(dev, int(kd.lib().kd_layer_norm_bwd_workspace_bytes(T, d)), workspace)
