@@ -46,21 +46,33 @@ int32_t norm_bwd_launch(const NormBwdArgs& A, hipStream_t st) {
 }
 
 // The narrowest variant that holds a row: NV vectors of 8 elements per lane,
-// WPR waves per row.
-#define KD_NORM_VARIANTS(FN)                                       \
-  if (A.d <= 512) return FN<T, WT, 1, 1>(A, st);                   \
-  if (A.d <= 1024) return FN<T, WT, 1, 2>(A, st);                  \
-  if (A.d <= 2048) return FN<T, WT, 1, 4>(A, st);                  \
-  if (A.d <= kNormWaveMax) return FN<T, WT, 1, 6>(A, st);          \
-  if (A.d <= 4096) return FN<T, WT, 4, 2>(A, st);                  \
-  if (A.d <= 8192) return FN<T, WT, 4, 4>(A, st);                  \
-  if (A.d <= 16384) return FN<T, WT, 16, 2>(A, st);                \
-  return FN<T, WT, 16, 4>(A, st);
-
+// WPR waves per row (norm_wpr in the plan).  The backward spreads rows wider
+// than 1024 over two waves and more: its accumulators take as many registers
+// as two rows, and with one wave per row of 2880 they left room for two waves
+// per SIMD and no row loaded ahead (128K rows from 8 bits: 527 us, against
+// the figure in kd_norm.hpp).
 template <class T, class WT>
-int32_t norm_fwd(const NormFwdArgs& A, hipStream_t st) { KD_NORM_VARIANTS(norm_fwd_launch) }
+int32_t norm_fwd(const NormFwdArgs& A, hipStream_t st) {
+  if (A.d <= 512) return norm_fwd_launch<T, WT, 1, 1>(A, st);
+  if (A.d <= 1024) return norm_fwd_launch<T, WT, 1, 2>(A, st);
+  if (A.d <= 2048) return norm_fwd_launch<T, WT, 1, 4>(A, st);
+  if (A.d <= 6 * 512) return norm_fwd_launch<T, WT, 1, 6>(A, st);
+  if (A.d <= 4096) return norm_fwd_launch<T, WT, 4, 2>(A, st);
+  if (A.d <= 8192) return norm_fwd_launch<T, WT, 4, 4>(A, st);
+  if (A.d <= 16384) return norm_fwd_launch<T, WT, 16, 2>(A, st);
+  return norm_fwd_launch<T, WT, 16, 4>(A, st);
+}
 template <class T, class WT>
-int32_t norm_bwd(const NormBwdArgs& A, hipStream_t st) { KD_NORM_VARIANTS(norm_bwd_launch) }
+int32_t norm_bwd(const NormBwdArgs& A, hipStream_t st) {
+  if (A.d <= 512) return norm_bwd_launch<T, WT, 1, 1>(A, st);
+  if (A.d <= 1024) return norm_bwd_launch<T, WT, 1, 2>(A, st);
+  if (A.d <= 2048) return norm_bwd_launch<T, WT, 2, 2>(A, st);
+  if (A.d <= 6 * 512) return norm_bwd_launch<T, WT, 2, 3>(A, st);
+  if (A.d <= 4096) return norm_bwd_launch<T, WT, 4, 2>(A, st);
+  if (A.d <= 8192) return norm_bwd_launch<T, WT, 4, 4>(A, st);
+  if (A.d <= 16384) return norm_bwd_launch<T, WT, 16, 2>(A, st);
+  return norm_bwd_launch<T, WT, 16, 4>(A, st);
+}
 
 int32_t norm_check(int32_t dtype, int32_t w_dtype, int64_t T, int64_t d) {
   if (!known_dtype(dtype) || !known_dtype(w_dtype) || (dtype == KD_F32 && w_dtype != KD_F32)) return KD_ERR_DTYPE;

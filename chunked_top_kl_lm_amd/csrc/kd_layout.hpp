@@ -27,7 +27,6 @@ constexpr int kMergeStrips = 64;   // strips merged per first-level logsumexp gr
 constexpr int kBlockRows = 32;     // cache builder: vocabulary rows per block maximum
 constexpr int kFbBatch = 1024;     // cache builder: ids per batch of the exact fallback
 constexpr int kActBlock = 128;     // 8-bit checkpoints: elements of a row that share a scale
-constexpr int kNormWaveMax = 6 * 512; // layer norm: widest row that one wave holds
 constexpr int kSampleSeg = 16384;  // sampling: ids of one block of the scan
 constexpr int kSampleBins = 2048;  // sampling: bins of T/64 below the largest logit; the last holds the rest
 constexpr int kSampleList = 4096;  // sampling: longest candidate list

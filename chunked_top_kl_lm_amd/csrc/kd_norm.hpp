@@ -9,13 +9,14 @@
 //
 // Both are bound by HBM: the forward reads x and writes y, the backward reads
 // dy and x (or its bytes) and writes dx; w and b stay in the caches.  A row
-// is held in registers between its statistics and its output, so it is read
-// once and the variance is the two-pass one (no cancellation).  Rows up to
-// kNormWaveMax elements belong to one wave: all reductions are lane exchanges, no
-// barrier; wider rows are spread over four or sixteen waves.
+// is held in registers, packed as it was loaded, between its statistics and
+// its output, so it is read once and the variance is the two-pass one (no
+// cancellation).  Narrow rows belong to one wave (the forward's up to 6 * 512,
+// the backward's up to 1024 elements): all reductions are lane exchanges, no
+// barrier; wider rows are spread over two, four or sixteen waves.
 //
 // The weight gradient: each lane owns fixed columns and adds its rows' terms
-// in fp32 registers; a block's waves are joined in LDS and a block writes one
+// in fp32 registers; a block's rows are joined in LDS and a block writes one
 // partial row; a second kernel adds the partial rows.  Everything runs in a
 // fixed order, so the results are the same bits from call to call.
 #pragma once
@@ -25,6 +26,13 @@
 #include "kd_act8.hpp"
 
 namespace kd {
+
+// Rows per block of threads and its size: four waves, or one row of sixteen.
+template <int WPR> struct NormCfg {
+  static constexpr int kRows = WPR < 4 ? 4 / WPR : 1;
+  static constexpr int kWaves = WPR * kRows;
+  static constexpr int kThreads = 64 * kWaves;
+};
 
 // Statistics over a row spread over WPR waves: sums, left in every lane.
 // s_red: one float2 per wave of the block, rewritten per call (the caller's
@@ -40,21 +48,16 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* s_red) {
     a = b = 0.f;
 #pragma unroll
     for (int i = 0; i < WPR; ++i) {
-      a += s_red[i].x;
-      b += s_red[i].y;
+      const float2 v = s_red[w / WPR * WPR + i];
+      a += v.x;
+      b += v.y;
     }
   }
   return make_float2(a, b);
 }
-
-// Rows per block of threads and its size: four single-wave rows, or one row.
-template <int WPR> struct NormCfg {
-  static constexpr int kRows = WPR == 1 ? 4 : 1;
-  static constexpr int kThreads = 64 * WPR * kRows;
-};
 // Vectors of a row that every lane holds in each variant (a variant serves
 // rows wider than the next narrower one's); of the others a lane may have none.
-constexpr int norm_whole(int NV) { return NV == 6 ? 4 : NV / 2; }
+constexpr int norm_whole(int NV) { return NV == 6 ? 4 : NV == 3 ? 2 : NV / 2; }
 
 // The row's columns: lane vectors of eight up to d8 = d rounded down to a
 // multiple of 8, then up to seven single columns that lanes 0 .. tail - 1 of
@@ -68,7 +71,7 @@ struct NormCols {
   bool owner;                                      // (uniform per wave) has the tail
   __device__ __forceinline__ explicit NormCols(int d_) : d(d_), d8(d_ & ~7), tail(d_ & 7) {
     lane = threadIdx.x & 63;
-    const int wave = WPR == 1 ? 0 : (int)(threadIdx.x >> 6);
+    const int wave = (int)(threadIdx.x >> 6) % WPR;
     c0 = 8 * (64 * wave + lane);
     owner = tail > 0 && (d8 / 512) % WPR == wave;
   }
@@ -115,8 +118,9 @@ struct NormFwdArgs {
 
 template <class T, class WT, int WPR, int NV, bool CKPT>
 __global__ __launch_bounds__(NormCfg<WPR>::kThreads) void norm_fwd_kernel(NormFwdArgs A) {
-  __shared__ float2 s_red[2][WPR];
+  __shared__ float2 s_red[2][NormCfg<WPR>::kWaves];
   constexpr int R = NormCfg<WPR>::kRows;
+  static_assert(WPR == 1 || R == 1, "rows of one block advance together");
   const NormCols<WPR, NV> C(A.d);
   const int wave = threadIdx.x >> 6, d = A.d;
   // one row per wave (or block) and launch; the loop only serves row counts
@@ -208,19 +212,24 @@ struct NormBwdArgs {
 
 // Rows of sixteen waves and four vectors (wider than 16384) are not held in
 // registers beside the accumulators: their second pass reads them again from
-// the L2.
+// the L2.  (Loading the next row ahead of each row's work, for 28 registers
+// more, measured slower: 479 against 464 us for 128K rows of 2880 from 8 bits.)
 template <int WPR, int NV> constexpr bool norm_hold() { return WPR * NV < 64; }
 
 // Blocks of rows in turn: block b takes rows b, b + grid, ... (times kRows).
 template <class T, class WT, int WPR, int NV, bool CKPT>
 __global__ __launch_bounds__(NormCfg<WPR>::kThreads) void norm_bwd_kernel(NormBwdArgs A) {
   typedef typename std::conditional<CKPT, int8_t, T>::type XT;
+  typedef NormCfg<WPR> Cfg;
   constexpr bool HOLD = norm_hold<WPR, NV>();
-  __shared__ float2 s_red[2][WPR];
-  __shared__ float s_acc[WPR == 1 ? 2 * NV * 512 + 16 : 1];
-  constexpr int R = NormCfg<WPR>::kRows;
+  constexpr int R = Cfg::kRows;
+  __shared__ float2 s_red[2][Cfg::kWaves];
+  __shared__ float s_acc[R > 1 ? 2 * NV * 512 * WPR + 16 : 1];
   const NormCols<WPR, NV> C(A.d);
-  const int wave = threadIdx.x >> 6, lane = C.lane, d = A.d;
+  const int lane = C.lane, d = A.d;
+  // row of the block, wave of the row (uniform per wave)
+  const int slot = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) / WPR);
+  const int wr = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) % WPR);
   Vec8 aw[NV], ab[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -231,116 +240,146 @@ __global__ __launch_bounds__(NormCfg<WPR>::kThreads) void norm_bwd_kernel(NormBw
   const float inv_d = 1.f / (float)d;
   const int64_t ldx = CKPT ? (int64_t)d : A.ldx;
   const XT* xb = CKPT ? (const XT*)A.q : (const XT*)A.x;
-  for (int64_t t = (int64_t)blockIdx.x * R + (R > 1 ? wave : 0); t < A.T; t += (int64_t)gridDim.x * R) {
-    const float mean = A.mean[t], rstd = A.rstd[t];
+
+  struct Row {
     Raw8<XT> x[NV];
     Raw8<T> dy[NV];
-    float sc[NV];
-    const T* dyr = (const T*)A.dy + t * (int64_t)d;
-    const XT* xr = xb + t * ldx;
-    const float* sr = CKPT ? A.scale + t * A.nb : nullptr;
-    auto load = [&](int i) {
-      dy[i] = C.load(dyr, i);
-      x[i] = C.load(xr, i);
-      sc[i] = 1.f;
-      if constexpr (CKPT) sc[i] = C.has(i) ? sr[C.col(i) / kActBlock] : 0.f;
-    };
+    float sc[NV], mean, rstd, xt, gt;
+  };
+  auto load_vec = [&](Row& r, int64_t t, int i) {
+    r.dy[i] = C.load((const T*)A.dy + t * (int64_t)d, i);
+    r.x[i] = C.load(xb + t * ldx, i);
+    r.sc[i] = 1.f;
+    if constexpr (CKPT) r.sc[i] = C.has(i) ? A.scale[t * A.nb + C.col(i) / kActBlock] : 0.f;
+  };
+  // (a slot past the last row gets the last row's loads and adds nothing)
+  auto load_row = [&](Row& r, int64_t t) {
+    r.mean = A.mean[t];
+    r.rstd = A.rstd[t];
     if constexpr (HOLD) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) load(i);
+      for (int i = 0; i < NV; ++i) load_vec(r, t, i);
     }
-    float xt = 0.f, gt = 0.f, wt = 0.f;
+    r.xt = r.gt = 0.f;
     if (C.owner) {
-      gt = C.load_tail(dyr);
-      wt = C.load_tail((const WT*)A.w);
-      xt = C.load_tail(xr);
-      if constexpr (CKPT) xt *= sr[C.d8 / kActBlock];
-      xt = (xt - mean) * rstd;
+      r.gt = C.load_tail((const T*)A.dy + t * (int64_t)d);
+      r.xt = C.load_tail(xb + t * ldx);
+      if constexpr (CKPT) r.xt *= A.scale[t * A.nb + C.d8 / kActBlock];
     }
-    // where a lane has no column, dy and w are zero, so every term below is too
+  };
+  auto row = [&](Row& r, int64_t t, bool live) {
+    // xh = x rstd - mean rstd in one step: off by a few roundings of |x| and
+    // |mean| over the deviation, as the rounding of mean alone is.  Where a
+    // lane has no column, dy and w are zero, so every term below is too.
+    const float rstd = r.rstd, shift = -r.mean * rstd;
     auto xhat = [&](int i) {
-      Vec8 v = unpack(x[i]);
+      Vec8 v = unpack(r.x[i]);
+      const float step = CKPT ? r.sc[i] * rstd : rstd;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v.v[e] = ((CKPT ? v.v[e] * sc[i] : v.v[e]) - mean) * rstd;
+      for (int e = 0; e < 8; ++e) v.v[e] = fmaf(v.v[e], step, shift);
       return v;
     };
-    awt = fmaf(gt, xt, awt);
-    abt += gt;
-    float sg = gt * wt, sgx = gt * wt * xt;
+    const float xt = C.has_tail() ? fmaf(r.xt, rstd, shift) : 0.f;
+    const float wt = C.owner ? C.load_tail((const WT*)A.w) : 0.f;
+    float sg = r.gt * wt, sgx = r.gt * wt * xt;
+    if (live) {
+      awt = fmaf(r.gt, xt, awt);
+      abt += r.gt;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if constexpr (!HOLD) load(i);
+      if constexpr (!HOLD) load_vec(r, t, i);
       const Vec8 w = unpack(C.load((const WT*)A.w, i));
-      const Vec8 g = unpack(dy[i]), xh = xhat(i);
+      const Vec8 g = unpack(r.dy[i]), xh = xhat(i);
+      if (live) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          aw[i].v[e] = fmaf(g.v[e], xh.v[e], aw[i].v[e]);
+          ab[i].v[e] += g.v[e];
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        aw[i].v[e] = fmaf(g.v[e], xh.v[e], aw[i].v[e]);
-        ab[i].v[e] += g.v[e];
         const float gw = g.v[e] * w.v[e];
         sg += gw;
         sgx = fmaf(gw, xh.v[e], sgx);
       }
-      // one vector at a time: the accumulators and the held row leave few
+      // one vector at a time: the accumulators and the held rows leave few
       // registers
       settle(aw[i]);
       settle(ab[i]);
       settle(sg, sgx);
+      if constexpr (!HOLD) asm volatile("" ::: "memory");        // the next vector's loads stay behind this one
     }
     const float2 m = row_sum2<WPR>(sg, sgx, s_red[flip]);
     flip ^= 1;
-    if (A.dx) {
-      const float mg = m.x * inv_d, mgx = m.y * inv_d;
+    if (A.dx && live) {
+      // dx = rstd (dy w) + t, t = -rstd (mean(g) + xh mean(g xh))
+      const float mg = -m.x * inv_d * rstd, mgx = -m.y * inv_d * rstd;
       T* dxr = (T*)A.dx + t * (int64_t)d;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (i >= norm_whole(NV) && i * C.S >= d) break;
         if constexpr (HOLD) {
-          keep(dy[i]);
-          keep(x[i]);
+          keep(r.dy[i]);
+          keep(r.x[i]);
         } else {
-          load(i);
+          load_vec(r, t, i);
         }
         const Vec8 w = unpack(C.load((const WT*)A.w, i));
-        const Vec8 g = unpack(dy[i]);
+        const Vec8 g = unpack(r.dy[i]);
         Vec8 o = xhat(i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = rstd * (fmaf(g.v[e], w.v[e], -mg) - o.v[e] * mgx);
+        for (int e = 0; e < 8; ++e) o.v[e] = fmaf(g.v[e] * w.v[e], rstd, fmaf(o.v[e], mgx, mg));
         C.store(dxr, i, o);
+        if constexpr (!HOLD) asm volatile("" ::: "memory");
       }
-      if (C.owner) C.store_tail(dxr, rstd * (fmaf(gt, wt, -mg) - xt * mgx));
+      if (C.owner) C.store_tail(dxr, fmaf(r.gt * wt, rstd, fmaf(xt, mgx, mg)));
     }
+  };
+
+  // the block's rows advance together (the barrier of row_sum2)
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t t = (int64_t)blockIdx.x * R;
+  auto at = [&](int64_t base) { return min(base + slot, A.T - 1); };
+  for (; t < A.T; t += step) {
+    Row r;
+    load_row(r, at(t));
+    row(r, at(t), t + slot < A.T);
   }
+
   if (!A.part) return;
   float* pw = A.part + (int64_t)blockIdx.x * 2 * d;
-  if constexpr (WPR == 1) {
-    // join the four waves' columns, in the order of the waves
-    float* s_tail = s_acc + 2 * NV * 512;
-    for (int w = 0; w < 4; ++w) {
-      if (wave == w) {
+  if constexpr (R > 1) {
+    // join the slots' columns, in their order
+    constexpr int H = NV * 512 * WPR;              // floats per sum
+    float* s_tail = s_acc + 2 * H;
+    for (int q = 0; q < R; ++q) {
+      if (slot == q) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            // element e of column group (i, lane) at [i][e][lane]: no bank conflicts
-            const int at = (i * 8 + e) * 64 + lane;
-            s_acc[at] = w ? s_acc[at] + aw[i].v[e] : aw[i].v[e];
-            s_acc[NV * 512 + at] = w ? s_acc[NV * 512 + at] + ab[i].v[e] : ab[i].v[e];
+            // element e of column group (i, wave, lane) at [i][wave][e][lane]: no bank conflicts
+            const int k = ((i * WPR + wr) * 8 + e) * 64 + lane;
+            s_acc[k] = q ? s_acc[k] + aw[i].v[e] : aw[i].v[e];
+            s_acc[H + k] = q ? s_acc[H + k] + ab[i].v[e] : ab[i].v[e];
           }
         if (C.has_tail()) {
-          s_tail[lane] = w ? s_tail[lane] + awt : awt;
-          s_tail[8 + lane] = w ? s_tail[8 + lane] + abt : abt;
+          s_tail[lane] = q ? s_tail[lane] + awt : awt;
+          s_tail[8 + lane] = q ? s_tail[8 + lane] + abt : abt;
         }
       }
       __syncthreads();
     }
-    for (int i = wave; i < 2 * NV; i += 4) {
+    for (int k = threadIdx.x >> 6; k < 2 * NV * WPR; k += Cfg::kWaves) {
       Vec8 o;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o.v[e] = s_acc[(i * 8 + e) * 64 + lane];
-      const int c = 512 * (i < NV ? i : i - NV) + 8 * lane;
-      if (c < C.d8) store8(pw + (i < NV ? 0 : d) + c, o);
+      for (int e = 0; e < 8; ++e) o.v[e] = s_acc[(k * 8 + e) * 64 + lane];
+      const int c = 512 * (k % (NV * WPR)) + 8 * lane;
+      if (c < C.d8) store8(pw + (k < NV * WPR ? 0 : d) + c, o);
     }
-    if (wave == 0 && C.has_tail()) {
+    if (threadIdx.x < 64 && lane < C.tail) {
       pw[C.d8 + lane] = s_tail[lane];
       pw[d + C.d8 + lane] = s_tail[8 + lane];
     }

@@ -236,13 +236,15 @@ inline int32_t make_cache_plan(int64_t T, int64_t d, int64_t V, int64_t K, int64
 // Operators around the head (see kd_norm.hpp, kd_logits.hpp, kd_sample.hpp)
 // ---------------------------------------------------------------------------
 
-// Layer norm backward: blocks of rows, one partial weight-gradient row each.
-// Two blocks of four waves fit a CU (the accumulators take about 230
-// registers at d = 2880); fewer rows per wave than two would spend as much on
-// the partial rows as on the data.
+// Layer norm backward: blocks of four waves (sixteen for rows wider than
+// 8192), one partial weight-gradient row each.  Up to a block per CU as long
+// as there are rows; past that a block takes at least eight, so that the
+// partial rows stay a small part of the traffic, up to the blocks that run at
+// once (three per CU; two for 4097 .. 8192, one of sixteen waves).
 inline int64_t norm_bwd_blocks(int64_t T, int64_t d) {
-  const int64_t rows = d <= kNormWaveMax ? 4 : 1;          // rows in flight per block
-  return std::max<int64_t>(1, std::min<int64_t>(2 * kNumCU, cdiv(T, 2 * rows)));
+  const int64_t rows = d <= 1024 ? 4 : d <= 6 * 512 ? 2 : 1;   // rows in flight per block
+  const int64_t most = (d <= 4096 ? 3 : d <= 8192 ? 2 : 1) * kNumCU;
+  return std::max<int64_t>(std::min<int64_t>(kNumCU, cdiv(T, rows)), std::min<int64_t>(most, T / 8));
 }
 inline size_t norm_bwd_workspace(int64_t T, int64_t d) {
   return align256((size_t)norm_bwd_blocks(T, d) * 2 * (size_t)d * sizeof(float));
