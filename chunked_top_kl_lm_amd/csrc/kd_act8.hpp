@@ -81,9 +81,9 @@ __device__ __forceinline__ void act8_store(const Vec8& x, int8_t* qrow, float* s
   const uint2 w = act8_pack(x, 1.0f / s);
   if (c + 8 <= d) {
     __builtin_memcpy(qrow + c, &w, 8);
-  } else {
+  } else if (c < d) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 7; ++i)
       if (c + i < d) qrow[c + i] = (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
   }
   if ((c & (kActBlock - 1)) == 0 && c < d) srow[c / kActBlock] = s;
@@ -91,81 +91,100 @@ __device__ __forceinline__ void act8_store(const Vec8& x, int8_t* qrow, float* s
 
 constexpr int kActRows = 4;       // rows (waves) of a block of threads
 constexpr int kActSpan = 512;     // elements of a row that a wave takes per load
-constexpr int kActLoads = 4;      // loads in flight
+constexpr int kActLoads = 4;      // most loads per wave, all in flight
 
-// Grid: x = groups of kActRows rows, y = spans of `per` * kActSpan elements
-// of each row.
-template <class T>
+// Grid: x = groups of kActRows rows, y = parts of PER * kActSpan elements of
+// each row.
+template <class T, int PER>
 __global__ __launch_bounds__(64 * kActRows) void act8_quantize_kernel(const T* x, int64_t ldx, int64_t rows, int d,
-                                                                      int per, int8_t* q, float* scale, int nb) {
+                                                                      int8_t* q, float* scale, int nb) {
   const int64_t t = (int64_t)blockIdx.x * kActRows + (threadIdx.x >> 6);
   if (t >= rows) return;                            // whole waves
   const T* xr = x + t * ldx;
   int8_t* qr = q + t * d;
   float* sr = scale + t * nb;
-  const int c0 = blockIdx.y * per * kActSpan, c1 = min(d, c0 + per * kActSpan);
-  for (int c = c0; c < c1; c += kActLoads * kActSpan) {
-    Vec8 v[kActLoads];
-    const int cl = c + 8 * (int)(threadIdx.x & 63);
+  const int c0 = blockIdx.y * PER * kActSpan, cl = c0 + 8 * (int)(threadIdx.x & 63);
+  Vec8 v[PER];
 #pragma unroll
-    for (int i = 0; i < kActLoads; ++i) v[i] = row_load8(xr, cl + i * kActSpan, c1);
+  for (int i = 0; i < PER; ++i) v[i] = row_load8(xr, cl + i * kActSpan, d);
 #pragma unroll
-    for (int i = 0; i < kActLoads; ++i)
-      if (c + i * kActSpan < c1) act8_store(v[i], qr, sr, cl + i * kActSpan, c1);
-  }
+  for (int i = 0; i < PER; ++i)
+    if (c0 + i * kActSpan < d) act8_store(v[i], qr, sr, cl + i * kActSpan, d);
 }
 
 // Back to x' (rounded to the output's type).  Rows of ldo elements; with
 // rows_pad > rows or ldo > d the padding is written with zeros (what the
 // matrix products read).
-template <class T>
+template <class T, int PER>
 __global__ __launch_bounds__(64 * kActRows) void act8_dequantize_kernel(const int8_t* q, const float* scale, int nb,
-                                                                        int64_t rows, int d, int per, T* out,
-                                                                        int64_t ldo, int64_t rows_pad) {
+                                                                        int64_t rows, int d, T* out, int64_t ldo,
+                                                                        int64_t rows_pad) {
   const int64_t t = (int64_t)blockIdx.x * kActRows + (threadIdx.x >> 6);
   if (t >= rows_pad) return;
-  const bool live = t < rows;
-  const int8_t* qr = q + (live ? t : 0) * d;
-  const float* sr = scale + (live ? t : 0) * nb;
+  const int dl = t < rows ? d : 0;                  // a padding row has no elements
+  const int8_t* qr = q + (t < rows ? t : 0) * d;
+  const float* sr = scale + (t < rows ? t : 0) * nb;
   T* o = out + t * ldo;
-  const int c0 = blockIdx.y * per * kActSpan, c1 = min((int)ldo, c0 + per * kActSpan);
-  for (int c = c0; c < c1; c += kActLoads * kActSpan) {
-    Vec8 v[kActLoads];
-    float s[kActLoads];
-    const int cl = c + 8 * (int)(threadIdx.x & 63);
+  const int cl = blockIdx.y * PER * kActSpan + 8 * (int)(threadIdx.x & 63);
+  Vec8 v[PER];
+  float s[PER];
 #pragma unroll
-    for (int i = 0; i < kActLoads; ++i) {
-      const int ci = cl + i * kActSpan;
-      v[i] = row_load8(qr, ci, live ? min(d, c1) : 0);
-      s[i] = live && ci < d ? sr[ci / kActBlock] : 0.f;
+  for (int i = 0; i < PER; ++i) {
+    const int c = cl + i * kActSpan;
+    v[i] = row_load8(qr, c, dl);
+    s[i] = c < dl ? sr[c / kActBlock] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = cl + i * kActSpan;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i].v[e] *= s[i];
+    if (c + 8 > dl && c < dl) {                     // the vector that crosses the row's end: zeros stay zeros
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i].v[e] = c + e < dl ? v[i].v[e] : 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < kActLoads; ++i) {
-      const int ci = cl + i * kActSpan;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i].v[e] = ci + e < d ? v[i].v[e] * s[i] : 0.f;
-      row_store8(o, ci, c1, v[i]);
-    }
+    row_store8(o, c, (int)ldo, v[i]);
   }
 }
 
-// Spans of a row that the grid's y covers, and loads per span: spans of up
-// to kActLoads loads, of equal length.
-inline void act8_spans(int64_t d, unsigned* spans, int* per) {
+// Parts of a row that the grid's y covers, and loads per part: as few parts
+// of up to kActLoads loads as hold the row, of equal length.
+inline void act8_parts(int64_t d, unsigned* parts, int* per) {
   const int64_t n = (d + kActSpan - 1) / kActSpan;
-  *spans = (unsigned)((n + kActLoads - 1) / kActLoads);
-  *per = (int)((n + *spans - 1) / *spans);
+  *parts = (unsigned)((n + kActLoads - 1) / kActLoads);
+  *per = (int)((n + *parts - 1) / *parts);
+}
+inline unsigned act8_groups(int64_t rows) { return (unsigned)((rows + kActRows - 1) / kActRows); }
+
+template <class T>
+void launch_act8_quantize(const T* x, int64_t ldx, int64_t rows, int64_t d, int8_t* q, float* scale, hipStream_t st) {
+  unsigned parts;
+  int per;
+  act8_parts(d, &parts, &per);
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(act8_groups(rows), parts), dim3(64 * kActRows), 0, st, x, ldx, rows, (int)d, q,
+                       scale, (int)((d + kActBlock - 1) / kActBlock));
+  };
+  if (per == 1) launch(act8_quantize_kernel<T, 1>);
+  else if (per == 2) launch(act8_quantize_kernel<T, 2>);
+  else if (per == 3) launch(act8_quantize_kernel<T, 3>);
+  else launch(act8_quantize_kernel<T, 4>);
 }
 
 template <class T>
 void launch_act8_dequantize(const int8_t* q, const float* scale, int64_t rows, int64_t d, T* out, int64_t ldo,
                             int64_t rows_pad, hipStream_t st) {
-  unsigned spans;
+  unsigned parts;
   int per;
-  act8_spans(ldo, &spans, &per);
-  hipLaunchKernelGGL(act8_dequantize_kernel<T>, dim3((unsigned)((rows_pad + kActRows - 1) / kActRows), spans),
-                     dim3(64 * kActRows), 0, st, q, scale, (int)((d + kActBlock - 1) / kActBlock), rows, (int)d, per,
-                     out, ldo, rows_pad);
+  act8_parts(ldo, &parts, &per);
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(act8_groups(rows_pad), parts), dim3(64 * kActRows), 0, st, q, scale,
+                       (int)((d + kActBlock - 1) / kActBlock), rows, (int)d, out, ldo, rows_pad);
+  };
+  if (per == 1) launch(act8_dequantize_kernel<T, 1>);
+  else if (per == 2) launch(act8_dequantize_kernel<T, 2>);
+  else if (per == 3) launch(act8_dequantize_kernel<T, 3>);
+  else launch(act8_dequantize_kernel<T, 4>);
 }
 
 }  // namespace kd

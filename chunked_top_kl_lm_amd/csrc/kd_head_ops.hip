@@ -161,18 +161,9 @@ int32_t kd_act8_quantize(const void* x, int64_t ldx, int32_t dtype, int64_t T, i
   if (!kd::known_dtype(dtype)) return KD_ERR_DTYPE;
   if (T < 1 || d < 1 || ldx < d || T > (1ll << 24) || d > (1ll << 24)) return KD_ERR_BAD_SHAPE;
   if (kd::misaligned(x, kd::elem_bytes(dtype)) || kd::misaligned(scale, 4)) return KD_ERR_BAD_SHAPE;
-  unsigned spans;
-  int per;
-  kd::act8_spans(d, &spans, &per);
-  const dim3 grid((unsigned)kd::cdiv(T, kd::kActRows), spans), block(64 * kd::kActRows);
-  const int nb = (int)kd::cdiv(d, kd::kActBlock);
   hipStream_t st = (hipStream_t)stream;
-  if (dtype == KD_BF16)
-    hipLaunchKernelGGL(kd::act8_quantize_kernel<uint16_t>, grid, block, 0, st, (const uint16_t*)x, ldx, T, (int)d, per,
-                       q, scale, nb);
-  else
-    hipLaunchKernelGGL(kd::act8_quantize_kernel<float>, grid, block, 0, st, (const float*)x, ldx, T, (int)d, per, q,
-                       scale, nb);
+  if (dtype == KD_BF16) kd::launch_act8_quantize<uint16_t>((const uint16_t*)x, ldx, T, d, q, scale, st);
+  else kd::launch_act8_quantize<float>((const float*)x, ldx, T, d, q, scale, st);
   KD_LAUNCH_CHECK();
   return KD_OK;
 }

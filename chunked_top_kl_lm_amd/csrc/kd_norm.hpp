@@ -218,7 +218,8 @@ template <int WPR, int NV> constexpr bool norm_hold() { return WPR * NV < 64; }
 
 // Blocks of rows in turn: block b takes rows b, b + grid, ... (times kRows).
 template <class T, class WT, int WPR, int NV, bool CKPT>
-__global__ __launch_bounds__(NormCfg<WPR>::kThreads) void norm_bwd_kernel(NormBwdArgs A) {
+__global__ __launch_bounds__(NormCfg<WPR>::kThreads, (sizeof(T) == 2 && WPR < 16 && NV < 4 ? 4 : 1))
+void norm_bwd_kernel(NormBwdArgs A) {
   typedef typename std::conditional<CKPT, int8_t, T>::type XT;
   typedef NormCfg<WPR> Cfg;
   constexpr bool HOLD = norm_hold<WPR, NV>();

@@ -240,10 +240,10 @@ inline int32_t make_cache_plan(int64_t T, int64_t d, int64_t V, int64_t K, int64
 // 8192), one partial weight-gradient row each.  Up to a block per CU as long
 // as there are rows; past that a block takes at least eight, so that the
 // partial rows stay a small part of the traffic, up to the blocks that run at
-// once (three per CU; two for 4097 .. 8192, one of sixteen waves).
+// once (four per CU; two for 4097 .. 8192, one of sixteen waves).
 inline int64_t norm_bwd_blocks(int64_t T, int64_t d) {
   const int64_t rows = d <= 1024 ? 4 : d <= 6 * 512 ? 2 : 1;   // rows in flight per block
-  const int64_t most = (d <= 4096 ? 3 : d <= 8192 ? 2 : 1) * kNumCU;
+  const int64_t most = (d <= 4096 ? 4 : d <= 8192 ? 2 : 1) * kNumCU;
   return std::max<int64_t>(std::min<int64_t>(kNumCU, cdiv(T, rows)), std::min<int64_t>(most, T / 8));
 }
 inline size_t norm_bwd_workspace(int64_t T, int64_t d) {

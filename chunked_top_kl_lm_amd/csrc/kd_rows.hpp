@@ -61,19 +61,23 @@ __device__ __forceinline__ void narrow(float* p, float f) { *p = f; }
 // Elements c .. c + 7 of a row of d (zeros past its end).
 template <class T>
 __device__ __forceinline__ Vec8 row_load8(const T* row, int c, int d) {
-  if (c + 8 <= d) return load8(row + c);
-  Vec8 r;
+  Vec8 r = {};
+  if (c + 8 <= d) {
+    r = load8(row + c);
+  } else if (c < d) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r.v[i] = c + i < d ? widen(row[c + i]) : 0.f;
+    for (int i = 0; i < 7; ++i)
+      if (c + i < d) r.v[i] = widen(row[c + i]);
+  }
   return r;
 }
 template <class T>
 __device__ __forceinline__ void row_store8(T* row, int c, int d, const Vec8& x) {
   if (c + 8 <= d) {
     store8(row + c, x);
-  } else {
+  } else if (c < d) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 7; ++i)
       if (c + i < d) narrow(row + c + i, x.v[i]);
   }
 }
@@ -122,19 +126,6 @@ __device__ __forceinline__ void settle(Vec8& x) {
                "+v"(x.v[7]));
 }
 __device__ __forceinline__ void settle(float& a, float& b) { asm volatile("" : "+v"(a), "+v"(b)); }
-
-// Elements c .. c + 7 of a row of d; zeros past its end, element by element
-// where the vector crosses it.
-template <class T>
-__device__ __forceinline__ Raw8<T> raw_row_load8(const T* row, int c, int d) {
-  if (c + 8 <= d) return raw_load8(row + c);
-  T e[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = c + i < d ? row[c + i] : (T)0;
-  Raw8<T> r;
-  __builtin_memcpy(&r, e, sizeof(r));
-  return r;
-}
 
 // ---------------------------------------------------------------------------
 // Exchanges between the lanes of a wave, as register moves (DPP): a step
