@@ -93,17 +93,18 @@ constexpr int kActRows = 4;       // rows (waves) of a block of threads
 constexpr int kActSpan = 512;     // elements of a row that a wave takes per load
 constexpr int kActLoads = 4;      // most loads per wave, all in flight
 
-// Grid: x = groups of kActRows rows, y = parts of PER * kActSpan elements of
-// each row.
+// Grid: for each group of kActRows rows, its parts of PER * kActSpan elements
+// (neighbouring blocks read neighbouring memory).
 template <class T, int PER>
 __global__ __launch_bounds__(64 * kActRows) void act8_quantize_kernel(const T* x, int64_t ldx, int64_t rows, int d,
-                                                                      int8_t* q, float* scale, int nb) {
-  const int64_t t = (int64_t)blockIdx.x * kActRows + (threadIdx.x >> 6);
+                                                                      int8_t* q, float* scale, int nb, int parts) {
+  const int group = blockIdx.x / parts, part = blockIdx.x - group * parts;
+  const int64_t t = (int64_t)group * kActRows + (threadIdx.x >> 6);
   if (t >= rows) return;                            // whole waves
   const T* xr = x + t * ldx;
   int8_t* qr = q + t * d;
   float* sr = scale + t * nb;
-  const int c0 = blockIdx.y * PER * kActSpan, cl = c0 + 8 * (int)(threadIdx.x & 63);
+  const int c0 = part * PER * kActSpan, cl = c0 + 8 * (int)(threadIdx.x & 63);
   Vec8 v[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) v[i] = row_load8(xr, cl + i * kActSpan, d);
@@ -118,14 +119,15 @@ __global__ __launch_bounds__(64 * kActRows) void act8_quantize_kernel(const T* x
 template <class T, int PER>
 __global__ __launch_bounds__(64 * kActRows) void act8_dequantize_kernel(const int8_t* q, const float* scale, int nb,
                                                                         int64_t rows, int d, T* out, int64_t ldo,
-                                                                        int64_t rows_pad) {
-  const int64_t t = (int64_t)blockIdx.x * kActRows + (threadIdx.x >> 6);
+                                                                        int64_t rows_pad, int parts) {
+  const int group = blockIdx.x / parts, part = blockIdx.x - group * parts;
+  const int64_t t = (int64_t)group * kActRows + (threadIdx.x >> 6);
   if (t >= rows_pad) return;
   const int dl = t < rows ? d : 0;                  // a padding row has no elements
   const int8_t* qr = q + (t < rows ? t : 0) * d;
   const float* sr = scale + (t < rows ? t : 0) * nb;
   T* o = out + t * ldo;
-  const int cl = blockIdx.y * PER * kActSpan + 8 * (int)(threadIdx.x & 63);
+  const int cl = part * PER * kActSpan + 8 * (int)(threadIdx.x & 63);
   Vec8 v[PER];
   float s[PER];
 #pragma unroll
@@ -147,12 +149,20 @@ __global__ __launch_bounds__(64 * kActRows) void act8_dequantize_kernel(const in
   }
 }
 
-// Parts of a row that the grid's y covers, and loads per part: as few parts
+// Parts of a row, and loads per part: as few parts
 // of up to kActLoads loads as hold the row, of equal length.
 inline void act8_parts(int64_t d, unsigned* parts, int* per) {
   const int64_t n = (d + kActSpan - 1) / kActSpan;
   *parts = (unsigned)((n + kActLoads - 1) / kActLoads);
   *per = (int)((n + *parts - 1) / *parts);
+}
+// One launch covers all rows: its threads are counted in 32 bits.
+inline bool act8_fits(int64_t rows, int64_t d) {
+  if (rows < 1 || d < 1 || rows > (1ll << 24) || d > (1ll << 24)) return false;
+  unsigned parts;
+  int per;
+  act8_parts(d, &parts, &per);
+  return (rows + kActRows - 1) / kActRows * parts < (1ll << 24);
 }
 inline unsigned act8_groups(int64_t rows) { return (unsigned)((rows + kActRows - 1) / kActRows); }
 
@@ -162,8 +172,8 @@ void launch_act8_quantize(const T* x, int64_t ldx, int64_t rows, int64_t d, int8
   int per;
   act8_parts(d, &parts, &per);
   auto launch = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(act8_groups(rows), parts), dim3(64 * kActRows), 0, st, x, ldx, rows, (int)d, q,
-                       scale, (int)((d + kActBlock - 1) / kActBlock));
+    hipLaunchKernelGGL(kernel, dim3(act8_groups(rows) * parts), dim3(64 * kActRows), 0, st, x, ldx, rows, (int)d, q,
+                       scale, (int)((d + kActBlock - 1) / kActBlock), (int)parts);
   };
   if (per == 1) launch(act8_quantize_kernel<T, 1>);
   else if (per == 2) launch(act8_quantize_kernel<T, 2>);
@@ -178,8 +188,8 @@ void launch_act8_dequantize(const int8_t* q, const float* scale, int64_t rows, i
   int per;
   act8_parts(ldo, &parts, &per);
   auto launch = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(act8_groups(rows_pad), parts), dim3(64 * kActRows), 0, st, q, scale,
-                       (int)((d + kActBlock - 1) / kActBlock), rows, (int)d, out, ldo, rows_pad);
+    hipLaunchKernelGGL(kernel, dim3(act8_groups(rows_pad) * parts), dim3(64 * kActRows), 0, st, q, scale,
+                       (int)((d + kActBlock - 1) / kActBlock), rows, (int)d, out, ldo, rows_pad, (int)parts);
   };
   if (per == 1) launch(act8_dequantize_kernel<T, 1>);
   else if (per == 2) launch(act8_dequantize_kernel<T, 2>);

@@ -159,7 +159,7 @@ int32_t kd_act8_quantize(const void* x, int64_t ldx, int32_t dtype, int64_t T, i
                          void* stream) {
   if (!x || !q || !scale) return KD_ERR_NULL_ARG;
   if (!kd::known_dtype(dtype)) return KD_ERR_DTYPE;
-  if (T < 1 || d < 1 || ldx < d || T > (1ll << 24) || d > (1ll << 24)) return KD_ERR_BAD_SHAPE;
+  if (!kd::act8_fits(T, d) || ldx < d) return KD_ERR_BAD_SHAPE;
   if (kd::misaligned(x, kd::elem_bytes(dtype)) || kd::misaligned(scale, 4)) return KD_ERR_BAD_SHAPE;
   hipStream_t st = (hipStream_t)stream;
   if (dtype == KD_BF16) kd::launch_act8_quantize<uint16_t>((const uint16_t*)x, ldx, T, d, q, scale, st);
@@ -172,7 +172,7 @@ int32_t kd_act8_dequantize(const int8_t* q, const float* scale, int32_t dtype, i
                            void* stream) {
   if (!q || !scale || !out) return KD_ERR_NULL_ARG;
   if (!kd::known_dtype(dtype)) return KD_ERR_DTYPE;
-  if (T < 1 || d < 1 || T > (1ll << 24) || d > (1ll << 24)) return KD_ERR_BAD_SHAPE;
+  if (!kd::act8_fits(T, d)) return KD_ERR_BAD_SHAPE;
   if (kd::misaligned(out, kd::elem_bytes(dtype)) || kd::misaligned(scale, 4)) return KD_ERR_BAD_SHAPE;
   if (dtype == KD_BF16) kd::launch_act8_dequantize<uint16_t>(q, scale, T, d, (uint16_t*)out, d, T, (hipStream_t)stream);
   else kd::launch_act8_dequantize<float>(q, scale, T, d, (float*)out, d, T, (hipStream_t)stream);

@@ -133,7 +133,7 @@ int32_t kd_head_logits(const void* hidden, int64_t ldh, const void* W, int32_t i
  * times the kept mass.  temperature 0 takes the largest logit (lowest id).
  * -inf and NaN logits are never drawn; a row that has no others gets the
  * token -1 and the log-probability -inf.  Borders are decided in 64 bits; an
- * id whose probability is below 1.3e-14 of the largest is not drawn.
+ * id whose probability is below 1.3e-14 of the largest may count as zero.
  *  logits  device [R, V], row stride ldz, dtype
  *  u       device [R] float32 or (u_is_f64) float64, in [0, 1); values
  *          outside are taken as the nearest end, NaN as 0
