@@ -486,17 +486,34 @@ struct SamplePicker {
   }
 
   // All ids in bins <= b into s.key (unordered), if their groups are at most
-  // `most`; their number, or one past kSampleList if they do not fit.
+  // `most`; their number, or one past kSampleList if they do not fit.  The
+  // groups that hold them are left as bits in group_bits().
+  __device__ __forceinline__ uint64_t* group_bits() const { return s.aux; }          // one per group ..
+  __device__ __forceinline__ bool has_bits() const { return A.groups <= 64 * (kSampleList / 2); }   // .. if they fit half of aux
   __device__ __forceinline__ int gather(int b, int most) {
-    int* list = (int*)s.aux;                       // groups to read: 2 * kSampleList places
+    int* list = (int*)(s.aux + kSampleList / 2);   // groups to read: kSampleList places
     if (threadIdx.x == 0) s.n = s.n2 = 0;
     __syncthreads();
-    for_groups([&](int i, float g) {
-      if (bin(g) <= b) {
-        const int at = atomicAdd(&s.n2, 1);
-        if (at < 2 * kSampleList) list[at] = i;
+    const bool bits = has_bits();
+    for (int i = threadIdx.x; i - (int)threadIdx.x < A.groups; i += 4 * kSamplePick) {   // whole waves
+      float g[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = i + j * kSamplePick < A.groups ? gmax[i + j * kSamplePick] : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int gi = i + j * kSamplePick;
+        const bool in = g[j] > -INFINITY && bin(g[j]) <= b;
+        const unsigned long long w = __ballot(in);
+        if (bits && (gi & 63) == 0 && gi < A.groups) group_bits()[gi / 64] = w;
+        if (w) {
+          int at = 0;                              // one count per wave
+          if ((threadIdx.x & 63) == 0) at = atomicAdd(&s.n2, (int)__popcll(w));
+          at = __builtin_amdgcn_readfirstlane(at) +
+               (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(w >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)w, 0));
+          if (in && at < kSampleList) list[at] = gi;
+        }
       }
-    });
+    }
     __syncthreads();
     const int ng = s.n2;
     if (ng > most) return kSampleList + 1;
@@ -758,14 +775,16 @@ struct SamplePicker {
     // 32 ids per thread and step: a bit each for those in the border, whose
     // ids then go to the list (hardly any lane has more than two)
     constexpr int D = 32 / N;
+    const bool bits = has_bits();
     int* ids = (int*)s.key;
     for (int v = (int)threadIdx.x * N; v < A.V; v += kSamplePick * 32) {
+      // (of groups with an id that high: the others are not read)
       u32x4 u[D];
 #pragma unroll
       for (int j = 0; j < D; ++j) {
-        const int vj = v + j * kSamplePick * N;
-        if (vj + N <= A.V) __builtin_memcpy(&u[j], row + vj, 16);
-        else u[j] = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};   // NaN of both types: in no bin
+        const int vj = v + j * kSamplePick * N, g = vj / kSampleGroup;
+        u[j] = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};   // NaN of both types: in no bin
+        if (vj + N <= A.V && (!bits || (group_bits()[g / 64] >> (g & 63)) & 1)) __builtin_memcpy(&u[j], row + vj, 16);
       }
       uint32_t hits = 0;
 #pragma unroll
