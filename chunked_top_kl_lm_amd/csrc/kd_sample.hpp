@@ -108,29 +108,30 @@ __device__ __forceinline__ int sample_scan_mode(const SampleArgs& A, const Sampl
 // A logit as the operator sees it: NaN as -inf, -0 as +0.
 __device__ __forceinline__ float sample_logit(float x) { return fmaxf(x + 0.f, -INFINITY); }
 
-// exp((l - m) c64 / 64).  2^f on |f| <= 1/2 by the Taylor series of exp in
-// f ln 2 up to degree 12 (remainder 0.3466^13 / 13! < 2e-16).
-__device__ __forceinline__ double sample_weight(float l, float m, double c64) {
-  const double y0 = ((double)l - (double)m) * (c64 * (1.4426950408889634 / 64.0));
-  const double y = y0 > -64.0 ? y0 : -64.0;        // also NaN (inf - inf, inf * 0)
-  const double k = rint(y);
-  const double f = (y - k) * 0.6931471805599453;
-  double p = 1.0 / 479001600.0;
-  p = fma(p, f, 1.0 / 39916800.0);
-  p = fma(p, f, 1.0 / 3628800.0);
-  p = fma(p, f, 1.0 / 362880.0);
-  p = fma(p, f, 1.0 / 40320.0);
-  p = fma(p, f, 1.0 / 5040.0);
-  p = fma(p, f, 1.0 / 720.0);
-  p = fma(p, f, 1.0 / 120.0);
-  p = fma(p, f, 1.0 / 24.0);
-  p = fma(p, f, 1.0 / 6.0);
-  p = fma(p, f, 0.5);
-  p = fma(p, f, 1.0);
-  p = fma(p, f, 1.0);
+// exp(y / 64) for y <= 1 (0 below -64 * 64 ln 2, and for NaN): 2^k times 2^f,
+// |f| <= 1/2, by the Taylor series of exp in f ln 2 up to degree 12 (remainder
+// 0.3466^13 / 13! < 2e-16).
+__device__ __forceinline__ double exp_bins(double y) {
+  constexpr double c[13] = {1.0, 1.0, 1.0 / 2.0, 1.0 / 6.0, 1.0 / 24.0, 1.0 / 120.0, 1.0 / 720.0, 1.0 / 5040.0,
+                            1.0 / 40320.0, 1.0 / 362880.0, 1.0 / 3628800.0, 1.0 / 39916800.0, 1.0 / 479001600.0};
+  const double z0 = y * (1.4426950408889634 / 64.0);
+  const double z = z0 > -64.0 ? z0 : -64.0;        // also NaN (inf - inf, inf * 0)
+  const double k = rint(z);
+  const double f = (z - k) * 0.6931471805599453;
+  double p = c[12];
+#pragma unroll
+  for (int i = 11; i >= 0; --i) {
+    double ci = c[i];
+    if (i > 2) asm("" : "+s"(ci));                 // a scalar operand, not a vector register (1 and 1/2 are inline)
+    p = fma(p, f, ci);
+  }
   // times 2^k, k in [-64, 0], p in [0.7, 1.42]: the exponent field directly
   const double w = __longlong_as_double(__double_as_longlong(p) + (long long)(int)k * (1ll << 52));
-  return l == m ? 1.0 : (y0 > -64.0 ? w : 0.0);
+  return z0 > -64.0 ? w : 0.0;
+}
+// exp((l - m) c64 / 64), l <= m.
+__device__ __forceinline__ double sample_weight(float l, float m, double c64) {
+  return l == m ? 1.0 : exp_bins(((double)l - (double)m) * c64);
 }
 // exp(y / 64) for |y| <= 1.5 (a logit against its bin's edge): degree 6 in
 // y / 64, remainder 0.0235^7 / 7! < 1e-15.  The coefficients are held in
@@ -231,11 +232,37 @@ __global__ __launch_bounds__(kSampleScan) void sample_scan_kernel(SampleArgs A) 
   if (tid == 0) A.smax[at] = m;
   if (mode == kScanMass) {
     double s = 0.0;
-    if (m > -INFINITY) {
+    const float top = floorf(m * p.cb);
+    if (fabsf(top) < kSampleGrid) {                // (uniform)
+      // exp((l - m) / T) as the factor of the logit's bin, from a table, and
+      // the six terms of its place in the bin
+      double* factor = (double*)s_hist;
+      for (int i = tid; i < kSampleBins; i += kSampleScan)
+        factor[i] = i < kSampleBins - 1 ? exp_bins(fma((double)m, -p.c64, (double)top - (double)i + 1.0)) : 0.0;
+      __syncthreads();
+      const EdgeWeight weight;
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
-        for (int i = 0; i < N; ++i) s += sample_weight(x[j][i], m, p.c64);
+        for (int q = 0; q < N; q += 2) {
+          // two ids at a time: their polynomials interleave, and the kernel
+          // stays within 64 registers (eight waves per SIMD)
+          double w[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float b = floorf(x[j][q + i] * p.cb), d = top - b;
+            const double e = weight(fma((double)x[j][q + i], p.c64, -(double)(b + 1.f)));
+            const bool in = d < (float)(kSampleBins - 1);   // false for -inf
+            w[i] = in ? e * factor[in ? (int)d : 0] : 0.0;
+          }
+          s += w[0] + w[1];
+          asm volatile("" : "+v"(s));
+        }
+    } else if (m > -INFINITY) {
+      // (read again: few rows come here)
+#pragma unroll 1
+      for (int i = tid; i < kSampleSeg && seg * kSampleSeg + i < A.V; i += kSampleScan)
+        s += sample_weight(sample_logit(load_elem<E>(row + seg * kSampleSeg + i)), m, p.c64);
     }
     s = wave_sum(s);
     if (lane == 0) s_sum[wave] = s;
@@ -643,7 +670,7 @@ struct SamplePicker {
   // Mass of bin j of the row relative to the largest logit: its entries are
   // kept relative to the bin's upper edge, top - j + 1 on the grid.
   __device__ __forceinline__ double bin_factor(int j) const {
-    return exp(fma((double)m, -p.c64, (double)top - (double)j + 1.0) * (1.0 / 64.0));
+    return exp_bins(fma((double)m, -p.c64, (double)top - (double)j + 1.0));
   }
   __device__ __forceinline__ int seg_offset(int sg) const {
     // bins between the row's largest logit and the segment's
