@@ -267,12 +267,15 @@ def _layer_norm_function():
         @staticmethod
         def forward(ctx, x, weight, bias, eps, checkpoint):
             rows = x if x.dim() == 2 else (x.flatten(0, -2) if x.dim() > 2 else x[None])
+            if rows.dim() == 2 and (rows.stride(1) != 1 or rows.stride(0) < rows.shape[1]):
+                rows = rows.contiguous()         # transposed, or rows that share memory (a broadcast input)
             y, mean, rstd, *kept = layer_norm_fwd(rows, weight, bias, eps, checkpoint)
             ctx.save_for_backward(weight, mean, rstd, *(kept or (rows,)))
             ctx.shape, ctx.rows, ctx.bias_dtype = x.shape, rows.shape, None if bias is None else bias.dtype
             return y.view(x.shape)
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, dy):
             weight, mean, rstd, *kept = ctx.saved_tensors
             need_x, need_w, need_b = ctx.needs_input_grad[:3]
@@ -318,8 +321,8 @@ def head_logits(hidden, W, out=None, workspace=None):
     """Logits of the output head, hidden [T, d] times W [V, d] transposed, as
     float32 [T, V] (kd_head_logits): the form for decoding steps (few rows,
     W read once) and for scoring (many rows).  hidden and W bfloat16 or
-    float32; hidden's rows may be strided.  `out`: a contiguous float32
-    [T, V] CUDA tensor; `workspace`: a uint8 CUDA tensor of
+    float32; hidden's rows may be strided.  Not differentiable (training goes
+    through kd_topk_kl_loss).  `out`: a contiguous float32 [T, V] CUDA tensor; `workspace`: a uint8 CUDA tensor of
     head_logits_workspace_bytes(...) bytes."""
     import torch
     kd = _pkg()

@@ -143,6 +143,74 @@ def test_layer_norm_autograd(ckpt):
         assert abs(num - (_np(x.grad).reshape(-1, 96) * e).sum()) <= 1e-4 * np.abs(_np(x.grad).reshape(-1, 96) * e).sum()
 
 
+def test_layer_norm_autograd_of_broadcast_and_shared_inputs():
+    """A broadcast input's gradient is the sum over its copies; a weight used
+    twice gets both uses' gradients; transposed inputs are taken."""
+    import chunked_top_kl_lm_amd as kd
+    torch = _t()
+    g = torch.Generator().manual_seed(9)
+    x0, w = torch.randn(1, 40, generator=g).cuda().requires_grad_(), torch.randn(40, generator=g).cuda().requires_grad_()
+    dy = torch.randn(6, 40, generator=g).cuda()
+    y = kd.layer_norm(kd.layer_norm(x0.expand(6, 40), w), w)
+    y.backward(dy)
+    xr, wr = x0.detach().cpu().double().requires_grad_(), w.detach().cpu().double().requires_grad_()
+    ln = lambda v: torch.nn.functional.layer_norm(v, (40,), wr, None, 1e-5)  # noqa: E731
+    ln(ln(xr.expand(6, 40))).backward(dy.cpu().double())
+    # two fp32 norms of 40 columns, sums over 6 rows: about 200 roundings, and
+    # the second norm's 1 / deviation (here above 0.3) on the first one's error
+    assert rel_f(_np(x0.grad), xr.grad.numpy()) <= 1000 * U and rel_f(_np(w.grad), wr.grad.numpy()) <= 1000 * U
+    t = torch.randn(40, 5, generator=g).cuda()
+    assert torch.equal(kd.layer_norm(t.t(), w), kd.layer_norm(t.t().contiguous(), w))
+    # a second derivative is refused, not silently zero
+    v = torch.randn(3, 40, generator=g).cuda().requires_grad_()
+    gr, = torch.autograd.grad(kd.layer_norm(v, w).sum(), v, create_graph=True)
+    with pytest.raises(RuntimeError):
+        gr.sum().backward()
+
+
+def test_layer_norm_more_rows_than_one_launch_covers():
+    import chunked_top_kl_lm_amd as kd
+    T = 4 * (1 << 20) + 7
+    x, dy, w, b = _norm_inputs(T, 3, _t().bfloat16, 1)
+    y, mean, rstd, q, s = kd.layer_norm_fwd(x, w, b, EPS, checkpoint="int8")
+    rq, rs = o.act8(x.float().cpu().numpy())
+    assert np.array_equal(q.cpu().numpy(), rq) and np.array_equal(s.cpu().numpy(), rs)
+    _check_norm(x, dy, w, b, (y, mean, rstd, *kd.layer_norm_bwd(dy, x, w, mean, rstd)))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows come out as they do alone."""
+    import chunked_top_kl_lm_amd as kd
+    torch = _t()
+    T, d = 1100000, 2000
+    x = torch.empty(T, d, dtype=torch.bfloat16, device="cuda:0").normal_()
+    w, b = torch.rand(d, device="cuda:0"), torch.rand(d, device="cuda:0")
+    tail = slice(T - 37, T)
+    y, mean, rstd, q, s = kd.layer_norm_fwd(x, w, b, EPS, checkpoint="int8")
+    one = kd.layer_norm_fwd(x[tail], w, b, EPS, checkpoint="int8")
+    for a, c in zip((y, mean, rstd, q, s), one):
+        assert torch.equal(a[tail], c)
+    q2, s2 = kd.act8_quantize(x)
+    assert torch.equal(q2, q) and torch.equal(s2, s)
+    back = kd.act8_dequantize(q, s)
+    assert torch.equal(back[tail], kd.act8_dequantize(q[tail], s[tail]))
+    del back, q2, s2
+    dx = kd.layer_norm_bwd(y, (q, s), w, mean, rstd, need_dweight=False)[0]
+    assert torch.equal(dx[tail], kd.layer_norm_bwd(y[tail], (q[tail], s[tail]), w, mean[tail], rstd[tail], need_dweight=False)[0])
+    del x, y, q, s, dx
+    T, V, d = 11000, 201088, 64
+    h = torch.empty(T, d, dtype=torch.bfloat16, device="cuda:0").normal_()
+    W = torch.empty(V, d, dtype=torch.bfloat16, device="cuda:0").normal_()
+    z = kd.head_logits(h, W)
+    last = kd.head_logits(h[-128:], W)
+    assert torch.equal(z[-128:], last)
+    u = torch.rand(T, device="cuda:0")
+    for kw in (dict(), dict(top_k=50), dict(top_p=0.9)):
+        tok, lp = kd.sample(z, u, **kw)
+        t2, l2 = kd.sample(z[-37:], u[-37:], **kw)
+        assert torch.equal(tok[-37:], t2) and torch.equal(lp[-37:], l2)
+
+
 def test_layer_norm_special_rows():
     import chunked_top_kl_lm_amd as kd
     torch = _t()
@@ -279,7 +347,9 @@ def _check_sample(z, u, kw, rows=None):
 FILTERS = [dict(), dict(temperature=0.7), dict(top_k=1), dict(top_k=7), dict(top_k=50, top_p=0.9), dict(top_p=0.5),
            dict(top_p=0.97, temperature=1.3), dict(min_p=0.05), dict(min_p=0.3, top_p=0.8), dict(top_k=40, top_p=0.9, min_p=0.1),
            dict(top_k=3000), dict(top_k=3000, top_p=0.99), dict(temperature=0.0), dict(temperature=50.0, top_p=0.6),
-           dict(min_p=1e-6), dict(top_p=1e-9), dict(min_p=1.0)]
+           dict(min_p=1e-6), dict(top_p=1e-9), dict(min_p=1.0), dict(temperature=1e-30), dict(temperature=1e-30, top_p=0.4),
+           dict(temperature=1e-3, min_p=0.1), dict(temperature=1e4, top_p=0.3), dict(temperature=1e30, top_k=500, top_p=0.5),
+           dict(temperature=1e30, min_p=0.9), dict(top_k=4096), dict(top_p=0.999999)]
 
 
 @pytest.mark.parametrize("V", [1, 2, 63, 64, 65, 1000, 1024, 1025, 5000, 33001])
