@@ -71,7 +71,7 @@ int32_t norm_bwd(const NormBwdArgs& A, hipStream_t st) {
   if (A.d <= 4096) return norm_bwd_launch<T, WT, 4, 2>(A, st);
   if (A.d <= 8192) return norm_bwd_launch<T, WT, 4, 4>(A, st);
   if (A.d <= 16384) return norm_bwd_launch<T, WT, 16, 2>(A, st);
-  return norm_bwd_launch<T, WT, 16, 4>(A, st);
+  return norm_bwd_launch<T, WT, 8, 8>(A, st);
 }
 
 int32_t norm_check(int32_t dtype, int32_t w_dtype, int64_t T, int64_t d) {
@@ -126,9 +126,11 @@ int32_t logits_run(const LogitsPlan& P, const void* hidden, int64_t ldh, const v
     }
     const EpiStoreLogits epi{logits + t0 * V, V, (int)V, (int)n};
     const int64_t kbytes = P.d_p * E::kBytes;
-    const hipError_t e =
-        P.tall ? launch_gemm<TileLogits, E>(make_shape<TileLogits>(w, ldw, (int)V, h, ld, (int)n, kbytes, 1, 1), epi, st)
-               : launch_gemm<TileMain, E>(make_shape<TileMain>(w, ldw, (int)V, h, ld, (int)n, kbytes, 1, 1), epi, st);
+    auto launch = [&](auto tile) {
+      typedef decltype(tile) TC;
+      return launch_gemm<TC, E>(make_shape<TC>(w, ldw, (int)V, h, ld, (int)n, kbytes, 1, 1), epi, st);
+    };
+    const hipError_t e = P.low ? launch(TileLogitsLow()) : P.tall ? launch(TileLogits()) : launch(TileMain());
     if (e != hipSuccess) return KD_ERR_HIP;
   }
   return KD_OK;

@@ -13,7 +13,7 @@
 // its output, so it is read once and the variance is the two-pass one (no
 // cancellation).  Narrow rows belong to one wave (the forward's up to 6 * 512,
 // the backward's up to 1024 elements): all reductions are lane exchanges, no
-// barrier; wider rows are spread over two, four or sixteen waves.
+// barrier; wider rows are spread over two to sixteen waves.
 //
 // The weight gradient: each lane owns fixed columns and adds its rows' terms
 // in fp32 registers; a block's rows are joined in LDS and a block writes one
@@ -210,7 +210,7 @@ struct NormBwdArgs {
   float* part;         // [blocks][2][d] partial dw and db, or NULL
 };
 
-// Rows of sixteen waves and four vectors (wider than 16384) are not held in
+// Rows of eight vectors per lane (wider than 16384) are not held in
 // registers beside the accumulators: their second pass reads them again from
 // the L2.  (Loading the next row ahead of each row's work, for 28 registers
 // more, measured slower: 479 against 464 us for 128K rows of 2880 from 8 bits.)
@@ -218,7 +218,7 @@ template <int WPR, int NV> constexpr bool norm_hold() { return WPR * NV < 64; }
 
 // Blocks of rows in turn: block b takes rows b, b + grid, ... (times kRows).
 template <class T, class WT, int WPR, int NV, bool CKPT>
-__global__ __launch_bounds__(NormCfg<WPR>::kThreads, (sizeof(T) == 2 && WPR < 16 && NV < 4 ? 4 : 1))
+__global__ __launch_bounds__(NormCfg<WPR>::kThreads, (sizeof(T) == 2 && sizeof(WT) == 2 && NV < 4 ? 4 : 1))
 void norm_bwd_kernel(NormBwdArgs A) {
   typedef typename std::conditional<CKPT, int8_t, T>::type XT;
   typedef NormCfg<WPR> Cfg;

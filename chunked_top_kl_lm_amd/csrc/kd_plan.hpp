@@ -37,7 +37,11 @@ using TileMain = TileCfg<256, 256, 2, 4, 2, 128>;
 using TileDhWide = TileCfg<256, 320, 4, 2, 2, 128>;
 using TileHead = TileCfg<256, 192, 4, 2, 2, 128>;
 using TileHeadNarrow = TileCfg<256, 128, 4, 2, 2, 128>;
-using TileLogits = TileCfg<320, 256, 2, 4, 2, 128>;      // 8 waves of 160 x 64
+//  - the logits of kd_head_logits: 256 x 256, or 320 x 256 (8 waves of 160 x
+//    64, 144 KB LDS) where that needs fewer rounds of the CUs, or for up to
+//    128 rows 128 x 128 (4 waves of 64 x 64, 64 KB LDS, two blocks per CU).
+using TileLogits = TileCfg<320, 256, 2, 4, 2, 128>;
+using TileLogitsLow = TileCfg<128, 128, 2, 2, 2, 128>;
 constexpr int kBM = TileMain::BM, kBN = TileMain::BN;
 constexpr int kWaveM = TileMain::BM / TileMain::WM;   // vocabulary strip of one LSE partial
 constexpr int kNumCU = 256;           // MI355X compute units (split-K sizing)
@@ -236,11 +240,11 @@ inline int32_t make_cache_plan(int64_t T, int64_t d, int64_t V, int64_t K, int64
 // Operators around the head (see kd_norm.hpp, kd_logits.hpp, kd_sample.hpp)
 // ---------------------------------------------------------------------------
 
-// Layer norm backward: blocks of four waves (sixteen for rows wider than
-// 8192), one partial weight-gradient row each.  Up to a block per CU as long
+// Layer norm backward: blocks of four waves (eight or sixteen for rows wider
+// than 8192), one partial weight-gradient row each.  Up to a block per CU as long
 // as there are rows; past that a block takes at least eight, so that the
 // partial rows stay a small part of the traffic, up to the blocks that run at
-// once (four per CU; two for 4097 .. 8192, one of sixteen waves).
+// once (four per CU; two for 4097 .. 8192, one of the wider).
 inline int64_t norm_bwd_blocks(int64_t T, int64_t d) {
   const int64_t rows = d <= 1024 ? 4 : d <= 6 * 512 ? 2 : 1;   // rows in flight per block
   const int64_t most = (d <= 4096 ? 4 : d <= 8192 ? 2 : 1) * kNumCU;
@@ -256,7 +260,7 @@ constexpr int64_t kSkinnyRows = 64;
 constexpr int64_t kLogitRows = 8192;
 struct LogitsPlan {
   bool skinny, pad_w, pad_h;
-  bool tall;          // 320-row tiles
+  bool low, tall;     // 128 x 128 tiles; 320-row tiles
   int64_t d_p, rows;
   size_t off_wp, off_hp, total;
 };
@@ -270,7 +274,12 @@ inline int32_t make_logits_plan(int64_t T, int64_t d, int64_t V, int32_t dt, boo
   p->skinny = T <= kSkinnyRows;
   p->d_p = round_up(d, 64);
   p->rows = std::min<int64_t>(T, kLogitRows);
-  // one block per CU: the time goes by whole rounds of kNumCU tiles
+  // up to 128 rows the product is bound by reading W and half of a 256-wide
+  // tile would be padding: 65 rows of d = 2880, V = 201088 take 274 us on 128 x
+  // 128 tiles and 306 on 320 x 256, 128 rows 296 and 306 (160 rows: 361, 313)
+  p->low = p->rows <= TileLogitsLow::BN;
+  // else one block per CU: the time goes by whole rounds of kNumCU tiles (512
+  // rows: 582 us on 256-row tiles, seven rounds, and 550 on 320-row ones, five)
   const int64_t cols = cdiv(p->rows, TileMain::BN);
   auto rounds = [&](int64_t bm) { return cdiv(cdiv(V, bm) * cols, kNumCU) * bm; };
   p->tall = rounds(TileLogits::BM) < rounds(TileMain::BM);

@@ -295,7 +295,7 @@ def test_loss_backward_from_8_bits(num, kw, chunk):
     assert max(e) <= 5e-2
 
 
-LOGIT_SHAPES = [(1, 1, 1), (1, 64, 1000), (3, 40, 17), (16, 257, 333), (17, 2880, 5000), (32, 96, 4096), (33, 64, 999), (64, 200, 5001), (65, 64, 640),
+LOGIT_SHAPES = [(1, 1, 1), (1, 64, 1000), (3, 40, 17), (16, 257, 333), (17, 2880, 5000), (32, 96, 4096), (33, 64, 999), (64, 200, 5001), (65, 64, 640), (128, 192, 1537), (129, 64, 700),
                 (100, 65, 1031), (256, 320, 2048), (300, 128, 70001), (1, 8193, 700), (64, 1000, 258)]
 
 
