@@ -239,8 +239,8 @@ int32_t kd_layer_norm_bwd(const void* dy, const void* x, int64_t ldx, const int8
 
 size_t kd_head_logits_workspace_bytes(int64_t T, int64_t d, int64_t V, int32_t in_dtype) {
   kd::LogitsPlan p;
-  // the size covers operands that do not start at multiples of 16 bytes
-  if (kd::make_logits_plan(T, d, V, in_dtype, d % 64 == 0, false, &p) != KD_OK) return 0;
+  // (covers a hidden whose rows do not start at multiples of 16 bytes)
+  if (kd::make_logits_plan(T, d, V, in_dtype, false, &p) != KD_OK) return 0;
   return p.total;
 }
 
@@ -250,9 +250,9 @@ int32_t kd_head_logits(const void* hidden, int64_t ldh, const void* W, int32_t i
   if (!kd::known_dtype(in_dtype)) return KD_ERR_DTYPE;
   const int64_t eb = kd::elem_bytes(in_dtype);
   kd::LogitsPlan p;
-  const int32_t rc = kd::make_logits_plan(T, d, V, in_dtype, kd::rows_aligned(W, d, eb),
-                                          kd::rows_aligned(hidden, ldh, eb), &p);
+  const int32_t rc = kd::make_logits_plan(T, d, V, in_dtype, kd::rows_aligned(hidden, ldh, eb), &p);
   if (rc != KD_OK) return rc;
+  if (!p.skinny && !p.pad_w && (((uintptr_t)W) & 15)) return KD_ERR_BAD_SHAPE;
   if (ldh < d || kd::misaligned(hidden, eb) || kd::misaligned(W, eb) || kd::misaligned(logits, 4)) return KD_ERR_BAD_SHAPE;
   if (p.total && (!workspace || workspace_bytes < p.total || (((uintptr_t)workspace) & 255))) return KD_ERR_WORKSPACE;
   hipStream_t st = (hipStream_t)stream;

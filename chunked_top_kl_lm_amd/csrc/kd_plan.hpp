@@ -254,9 +254,12 @@ inline size_t norm_bwd_workspace(int64_t T, int64_t d) {
   return align256((size_t)norm_bwd_blocks(T, d) * 2 * (size_t)d * sizeof(float));
 }
 
-// Head logits: rows up to kSkinnyRows take the product that reads W once;
-// more run on the GEMM, kLogitRows at a time.
-constexpr int64_t kSkinnyRows = 64;
+// Head logits: up to kSkinnyRows rows take the product that needs no operand
+// in any layout, twice as many where the GEMM would first have to copy W to a
+// padded width (aligned, 48 rows take 253 us on the GEMM's low tiles and 260
+// without; the copy alone moves W twice more); the rest run on the GEMM,
+// kLogitRows at a time.
+constexpr int64_t kSkinnyRows = 32;
 constexpr int64_t kLogitRows = 8192;
 struct LogitsPlan {
   bool skinny, pad_w, pad_h;
@@ -264,14 +267,13 @@ struct LogitsPlan {
   int64_t d_p, rows;
   size_t off_wp, off_hp, total;
 };
-// aligned_w / aligned_h: every row of W / hidden starts at a multiple of 16
-// bytes (and hidden's stride is within the GEMM's 32-bit tile offsets).
-inline int32_t make_logits_plan(int64_t T, int64_t d, int64_t V, int32_t dt, bool aligned_w, bool aligned_h,
-                                LogitsPlan* p) {
+// aligned_h: every row of hidden starts at a multiple of 16 bytes (and its
+// stride is within the GEMM's 32-bit tile offsets).
+inline int32_t make_logits_plan(int64_t T, int64_t d, int64_t V, int32_t dt, bool aligned_h, LogitsPlan* p) {
   if (dt != KD_BF16 && dt != KD_F32) return KD_ERR_DTYPE;
   if (T < 1 || d < 1 || V < 1 || T > (1ll << 24) || d > (1ll << 20) || V > (1ll << 24)) return KD_ERR_BAD_SHAPE;
   const int64_t eb = dt == KD_BF16 ? 2 : 4;
-  p->skinny = T <= kSkinnyRows;
+  p->skinny = T <= (d % 64 != 0 ? 2 : 1) * kSkinnyRows;
   p->d_p = round_up(d, 64);
   p->rows = std::min<int64_t>(T, kLogitRows);
   // up to 128 rows the product is bound by reading W and half of a 256-wide
@@ -283,7 +285,7 @@ inline int32_t make_logits_plan(int64_t T, int64_t d, int64_t V, int32_t dt, boo
   const int64_t cols = cdiv(p->rows, TileMain::BN);
   auto rounds = [&](int64_t bm) { return cdiv(cdiv(V, bm) * cols, kNumCU) * bm; };
   p->tall = rounds(TileLogits::BM) < rounds(TileMain::BM);
-  p->pad_w = !p->skinny && (d % 64 != 0 || !aligned_w);
+  p->pad_w = !p->skinny && d % 64 != 0;
   p->pad_h = !p->skinny && (d % 64 != 0 || !aligned_h);
   size_t o = 0;
   p->off_wp = o;

@@ -107,14 +107,15 @@ int32_t kd_topk_kl_bwd_act8(const int8_t* q, const float* scale, const void* W, 
  * Logits of the output head: z[t, v] = hidden[t] . W[v], fp32 sums of exact
  * products.
  *  hidden  device [T, d], row stride ldh, in_dtype
- *  W       device [V, d], in_dtype
+ *  W       device [V, d], in_dtype; 16-byte aligned (KD_ERR_BAD_SHAPE) unless
+ *          the call is one of few rows or d is not a multiple of 64
  *  logits  device [T, V] float32 (written)
- * A few rows (a decoding step) read W once and need no workspace; more rows
- * run on the library's matrix product, whose workspace holds zero-padded
- * copies of the operands where d is not a multiple of 64 (or a row of
- * hidden or W does not start at a multiple of 16 bytes):
- * kd_head_logits_workspace_bytes(...), 256-byte aligned, 0 if none is needed
- * (or the sizes are invalid).
+ * Up to 32 rows (a decoding step; 64 where d is not a multiple of 64) read W
+ * once and need no workspace; more rows run on the library's matrix product,
+ * whose workspace holds zero-padded copies of the operands where d is not a
+ * multiple of 64, and one of hidden where its rows do not start at multiples
+ * of 16 bytes: kd_head_logits_workspace_bytes(...), 256-byte aligned, 0 if
+ * none is needed (or the sizes are invalid).
  * 1 <= d <= 2^20, 1 <= V <= KD_HEAD_MAX_V, 1 <= T <= 2^24.
  */
 size_t kd_head_logits_workspace_bytes(int64_t T, int64_t d, int64_t V, int32_t in_dtype);

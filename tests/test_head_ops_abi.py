@@ -79,7 +79,7 @@ ACT8_BWD = dict(q=P, scale=P, W=P, dt=0, idx=P, logit=P, mask=None, T=64, d=64, 
     ("kd_head_logits", LOGITS, k, c) for k, c in
     [(dict(h=None), 1), (dict(W=None), 1), (dict(z=None), 1), (dict(dt=4), 5), (dict(T=0), 2), (dict(d=0), 2),
      (dict(V=0), 2), (dict(V=(1 << 24) + 1), 2), (dict(ldh=8), 2), (dict(h=P + 1), 2), (dict(z=P + 2), 2),
-     (dict(T=65, d=63), 6), (dict(T=65, d=63, ws=P + 16, wsb=1 << 30), 6), (dict(T=65, h=P + 2), 6)]
+     (dict(T=65, d=63), 6), (dict(T=65, d=63, ws=P + 16, wsb=1 << 30), 6), (dict(T=65, h=P + 2), 6), (dict(T=65, W=P + 4), 2)]
 ] + [
     ("kd_sample", SAMPLE, k, c) for k, c in
     [(dict(z=None), 1), (dict(u=None), 1), (dict(tok=None), 1), (dict(dt=2), 5), (dict(R=0), 2), (dict(V=0), 2),
