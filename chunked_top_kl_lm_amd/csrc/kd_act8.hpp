@@ -17,7 +17,10 @@
 // Bound by HBM: (e + 1 + 4/128) bytes per element each way, e the element's
 // size.  A lane takes eight consecutive elements, sixteen lanes a block, so
 // the block's maximum is four lane exchanges and no LDS; a wave takes up to
-// four blocks per load, several loads in flight.
+// four blocks per load, several loads in flight.  fp32 rows of 2880, 32768 of
+// them (475 MB a way): 111 us to bytes, 96 us back, 4.3 and 4.9 TB/s where a
+// copy of gigabytes reaches 4.7 (read and write counted); 2048 bf16 rows, in
+// the caches, 6 us each way.
 #pragma once
 
 #include "kd_layout.hpp"

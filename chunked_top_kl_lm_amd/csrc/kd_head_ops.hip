@@ -46,11 +46,9 @@ int32_t norm_bwd_launch(const NormBwdArgs& A, hipStream_t st) {
 }
 
 // The narrowest variant that holds a row: NV vectors of 8 elements per lane,
-// WPR waves per row (norm_wpr in the plan).  The backward spreads rows wider
-// than 1024 over two waves and more: its accumulators take as many registers
-// as two rows, and with one wave per row of 2880 they left room for two waves
-// per SIMD and no row loaded ahead (128K rows from 8 bits: 527 us, against
-// the figure in kd_norm.hpp).
+// WPR waves per row.  The backward spreads rows wider than 1024 over two waves
+// and more: its accumulators take as many registers as two rows, and with one
+// wave per row of 2880 they left room for two waves per SIMD (128K rows of 2880 from 8 bits: 527 us, with two waves 415).
 template <class T, class WT>
 int32_t norm_fwd(const NormFwdArgs& A, hipStream_t st) {
   if (A.d <= 512) return norm_fwd_launch<T, WT, 1, 1>(A, st);
@@ -95,7 +93,8 @@ int32_t logits_run(const LogitsPlan& P, const void* hidden, int64_t ldh, const v
     };
     // more waves share a block's hidden rows as these grow: at d = 2880, V =
     // 201088, 32 rows take 234 us with eight waves and 245 with four, 64 rows
-    // 278 and 284; one row 204 with four and 212 with eight
+    // (a d that the matrix product would need a copy of W for) 278 and 284; one
+    // row 204 with four and 212 with eight
     if (T <= 16) launch(skinny_logits_kernel<E, 1, 4>, 4);
     else if (T <= 32) launch(skinny_logits_kernel<E, 2, 8>, 8);
     else launch(skinny_logits_kernel<E, 4, 8>, 8);

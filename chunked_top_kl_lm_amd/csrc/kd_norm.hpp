@@ -13,7 +13,11 @@
 // its output, so it is read once and the variance is the two-pass one (no
 // cancellation).  Narrow rows belong to one wave (the forward's up to 6 * 512,
 // the backward's up to 1024 elements): all reductions are lane exchanges, no
-// barrier; wider rows are spread over two to sixteen waves.
+// barrier; wider rows are spread over two to sixteen waves.  131072 bf16 rows
+// of 2880 with checkpoints in 8 bits: forward 351 us (1.91 GB, 5.4 TB/s),
+// backward 415 us (1.91 GB, 4.6 TB/s) and 8 us for the partial rows, where a
+// copy of gigabytes reaches 4.7 (read and write counted); 8192 rows without
+// checkpoints 22 and 31 us, what of them the caches hold included.
 //
 // The weight gradient: each lane owns fixed columns and adds its rows' terms
 // in fp32 registers; a block's rows are joined in LDS and a block writes one
@@ -213,7 +217,8 @@ struct NormBwdArgs {
 // Rows of eight vectors per lane (wider than 16384) are not held in
 // registers beside the accumulators: their second pass reads them again from
 // the L2.  (Loading the next row ahead of each row's work, for 28 registers
-// more, measured slower: 479 against 464 us for 128K rows of 2880 from 8 bits.)
+// more, measured slower: 479 against 464 us for the kernel of then, 128K rows of
+// 2880 from 8 bits.)
 template <int WPR, int NV> constexpr bool norm_hold() { return WPR * NV < 64; }
 
 // Blocks of rows in turn: block b takes rows b, b + grid, ... (times kRows).
