@@ -137,17 +137,18 @@ constexpr int kDppHalfMirror = 0x141;   // lane i <- 7 - i of its eight
 constexpr int kDppMirror = 0x140;       // lane i <- 15 - i of its sixteen
 
 // The value of the lane that CTRL names; lanes that the move does not reach
-// (outside ROWS, or shifted in) get zero bits.
+// (outside ROWS, or shifted in) get zero bits.  (Where it reaches all, stated
+// as bound control, the compiler makes it one instruction with its user.)
 template <int CTRL, int ROWS = 0xf, class T>
 __device__ __forceinline__ T dpp(T v) {
   static_assert(sizeof(T) == 4 || sizeof(T) == 8, "one or two registers");
   if constexpr (sizeof(T) == 4) {
-    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, true));
   } else {
     const int2 u = __builtin_bit_cast(int2, v);
     int2 r;
-    r.x = __builtin_amdgcn_update_dpp(0, u.x, CTRL, ROWS, 0xf, false);
-    r.y = __builtin_amdgcn_update_dpp(0, u.y, CTRL, ROWS, 0xf, false);
+    r.x = __builtin_amdgcn_update_dpp(0, u.x, CTRL, ROWS, 0xf, true);
+    r.y = __builtin_amdgcn_update_dpp(0, u.y, CTRL, ROWS, 0xf, true);
     return __builtin_bit_cast(T, r);
   }
 }

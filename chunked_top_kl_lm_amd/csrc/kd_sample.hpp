@@ -20,8 +20,8 @@
 // and what the row's filters need: nothing (top_k), the segment's mass (no
 // filter), or a histogram of its mass over bins of T/64 (top_p, min_p).  The
 // bins lie on a grid of absolute logits, so that no block has to know the
-// row's largest logit; a bin's mass is kept relative to its upper edge, where
-// exp needs six terms only.
+// row's largest logit; a bin's mass is kept relative to its middle, where exp
+// needs five terms only.
 //
 // sample_pick_kernel (a block per row) then
 //  - finds from the group maxima (top_k) or from the joined histogram how far
@@ -78,7 +78,8 @@ struct SampleArgs {
 // id; min_p > 1: w = 1 only).
 struct SampleRow {
   double c64;        // 64 / T: logits in bins
-  float cb;          // the same, rounded: what bins are formed with
+  double step;       // T / 64: a bin in logits
+  float cb;          // c64, rounded: bins off the grid, parts of bins
   double top_p, min_p;
   int top_k;         // 0: off
   bool greedy;
@@ -94,6 +95,7 @@ __device__ __forceinline__ SampleRow sample_row(const SampleArgs& A, int r) {
   p.min_p = mp > 0.0 ? (mp < 1.0 ? mp : 1.0) : 0.0;
   p.greedy = !(t > 0.0) || p.top_k == 1 || p.top_p <= 0.0;
   p.c64 = 64.0 / t;
+  p.step = t * (1.0 / 64.0);
   p.cb = (float)p.c64;
   return p;
 }
@@ -133,25 +135,49 @@ __device__ __forceinline__ double exp_bins(double y) {
 __device__ __forceinline__ double sample_weight(float l, float m, double c64) {
   return l == m ? 1.0 : exp_bins(((double)l - (double)m) * c64);
 }
-// exp(y / 64) for |y| <= 1.5 (a logit against its bin's edge): degree 6 in
-// y / 64, remainder 0.0235^7 / 7! < 1e-15.  The coefficients are held in
+// The grid of bins: a logit l is in bin rint(l c64), counted from its row's or
+// segment's largest.  Added to 1.5 * 2^52 in one step, l c64 is rounded once,
+// to the integer in the sum's low bits, so bins are in the logits' order and
+// the same wherever they are formed.  Off for largest logits beyond `most`
+// bins, infinities, and temperatures so extreme that a bin's logits leave
+// fp32's range.
+struct SampleGrid {
+  static constexpr double kInt = 6755399441055744.0;
+  double c64;
+  bool on;
+  int top;           // bin of the largest logit
+  __device__ __forceinline__ SampleGrid(float m, const SampleRow& p, double most) : c64(p.c64) {
+    on = p.step > 0x1p-60 && p.step < 0x1p+60 && fabs((double)m * c64) < most;
+    top = on ? at(m) : 0;
+  }
+  __device__ __forceinline__ int at(float l) const { return (int)__double_as_longlong(fma((double)l, c64, kInt)); }
+  // The least logit of the bins 0 .. j below the largest one's: the border
+  // between two bins (b - 1/2) / c64, rounded to fp32, or its neighbour.
+  __device__ __forceinline__ float least(int j, double step) const {
+    const int b = top - j;
+    const float l = (float)(((double)b - 0.5) * step);        // not 0
+    const int up = l > 0.f ? 1 : -1;
+    const float below = __int_as_float(__float_as_int(l) - up), above = __int_as_float(__float_as_int(l) + up);
+    return at(below) >= b ? below : (at(l) >= b ? l : above);
+  }
+};
+// exp(y / 64) for |y| <= 1/2 (a logit against its bin's middle): degree 5 in
+// y / 64, remainder 0.0078^6 / 6! < 4e-16.  The coefficients are held in
 // scalar registers, so that a step of the polynomial is one instruction.
-struct EdgeWeight {
-  double c[6];
-  __device__ __forceinline__ EdgeWeight() {
+struct BinWeight {
+  double c[5];
+  __device__ __forceinline__ BinWeight() {
     constexpr double h = 1.0 / 64.0;
     c[0] = h;
     c[1] = h * h / 2.0;
     c[2] = h * h * h / 6.0;
     c[3] = h * h * h * h / 24.0;
     c[4] = h * h * h * h * h / 120.0;
-    c[5] = h * h * h * h * h * h / 720.0;
 #pragma unroll
-    for (int i = 0; i < 6; ++i) asm("" : "+s"(c[i]));
+    for (int i = 0; i < 5; ++i) asm("" : "+s"(c[i]));
   }
   __device__ __forceinline__ double operator()(double y) const {
-    double p = fma(c[5], y, c[4]);
-    p = fma(p, y, c[3]);
+    double p = fma(c[4], y, c[3]);
     p = fma(p, y, c[2]);
     p = fma(p, y, c[1]);
     p = fma(p, y, c[0]);
@@ -169,11 +195,11 @@ __device__ __forceinline__ uint64_t sample_units(double w, double scale) {
   return (uint64_t)__double_as_longlong(fma(w, scale, 4503599627370496.0)) - 0x4330000000000000ull;
 }
 
-// 16 bytes of consecutive logits of a row (-inf past its end).
+// 16 bytes of consecutive logits of a row (-inf past its end); RAW: NaN stays.
 template <class E> struct SampleVec;
 template <> struct SampleVec<Bf16> { static constexpr int N = 8; };
 template <> struct SampleVec<F32> { static constexpr int N = 4; };
-template <class E>
+template <class E, bool RAW = false>
 __device__ __forceinline__ void sample_load(const typename E::T* row, int v, int V, float* x) {
   constexpr int N = SampleVec<E>::N;
   if (v + N <= V) {
@@ -189,14 +215,47 @@ __device__ __forceinline__ void sample_load(const typename E::T* row, int v, int
     for (int i = 0; i < N; ++i) x[i] = v + i < V ? load_elem<E>(row + v + i) : -INFINITY;
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = sample_logit(x[i]);
+  for (int i = 0; i < N; ++i) x[i] = RAW ? x[i] + 0.f : sample_logit(x[i]);
 }
 
-// A block per row and segment; 32 ids per thread, held in registers.  Bound by
-// issue: some 36 vector instructions per id and lane, most of them the
-// polynomial's in doubles, and one LDS addition: 256 fp32 rows of 201088 with
-// top_p take 63 us (3.3 TB/s), of which the instructions alone are 47; a greedy
-// choice, which only reads, takes 35 with both kernels.
+// The larger of two numbers that are not signalling NaN; of a number and a
+// NaN the number.  (fmaxf quiets its arguments first: two instructions more.)
+__device__ __forceinline__ float quiet_max(float a, float b) {
+  float r;
+  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+// Each of g's values becomes the maximum over the 16 (eight values) or 8 lanes
+// (four) that share a group, by maxima whose second operand is another lane's:
+// those that a DPP reads were written three instructions before at least (two
+// are the least), the first ones by the wait.
+__device__ __forceinline__ void group_max(float (&g)[8]) {
+#define KD_STEP(c)                                                                                                   \
+  "v_max_f32_dpp %0, %0, %0 " c "\n\tv_max_f32_dpp %1, %1, %1 " c "\n\tv_max_f32_dpp %2, %2, %2 " c                  \
+  "\n\tv_max_f32_dpp %3, %3, %3 " c "\n\tv_max_f32_dpp %4, %4, %4 " c "\n\tv_max_f32_dpp %5, %5, %5 " c             \
+  "\n\tv_max_f32_dpp %6, %6, %6 " c "\n\tv_max_f32_dpp %7, %7, %7 " c "\n\t"
+  asm("s_nop 4\n\t" KD_STEP("quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf")
+      KD_STEP("quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf") KD_STEP("row_half_mirror row_mask:0xf bank_mask:0xf")
+      KD_STEP("row_mirror row_mask:0xf bank_mask:0xf")
+      : "+v"(g[0]), "+v"(g[1]), "+v"(g[2]), "+v"(g[3]), "+v"(g[4]), "+v"(g[5]), "+v"(g[6]), "+v"(g[7]));
+#undef KD_STEP
+}
+__device__ __forceinline__ void group_max(float (&g)[4]) {
+#define KD_STEP(c)                                                                                                   \
+  "v_max_f32_dpp %0, %0, %0 " c "\n\tv_max_f32_dpp %1, %1, %1 " c "\n\tv_max_f32_dpp %2, %2, %2 " c                  \
+  "\n\tv_max_f32_dpp %3, %3, %3 " c "\n\t"
+  asm("s_nop 4\n\t" KD_STEP("quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf")
+      KD_STEP("quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf") KD_STEP("row_half_mirror row_mask:0xf bank_mask:0xf")
+      : "+v"(g[0]), "+v"(g[1]), "+v"(g[2]), "+v"(g[3]));
+#undef KD_STEP
+}
+
+// A block per row and segment; 32 ids per thread, held in registers, 64
+// registers in all (full occupancy).  256 fp32 rows of 201088 with top_p from
+// HBM take 60 us (3.4 TB/s), 50 with neither masses nor histogram: reading
+// bounds it, a block's phases (read, largest logit, histogram, write) one
+// after the other keep it below a copy's rate.  Bins by fp32 products and
+// floors, with a polynomial of one more degree about the bin's edge, took 62.5.
 template <class E>
 __global__ __launch_bounds__(kSampleScan) void sample_scan_kernel(SampleArgs A) {
   constexpr int N = SampleVec<E>::N, L = kSampleSeg / (N * kSampleScan);
@@ -209,19 +268,23 @@ __global__ __launch_bounds__(kSampleScan) void sample_scan_kernel(SampleArgs A) 
   const typename E::T* row = (const typename E::T*)A.z + (int64_t)r * A.ldz;
   float x[L][N];
 #pragma unroll
-  for (int j = 0; j < L; ++j) sample_load<E>(row, seg * kSampleSeg + (j * kSampleScan + tid) * N, A.V, x[j]);
+  for (int j = 0; j < L; ++j) sample_load<E, true>(row, seg * kSampleSeg + (j * kSampleScan + tid) * N, A.V, x[j]);
   const SampleRow p = sample_row(A, r);
   const int mode = sample_scan_mode(A, p);
-  float m = -INFINITY;
+  static_assert(kSampleGroup / N == (L == 8 ? 16 : 8), "lanes of a group");
+  float m = -INFINITY, g[L];
 #pragma unroll
   for (int j = 0; j < L; ++j) {
-    float g = x[j][0];
+    g[j] = -INFINITY;                              // (stays where all are NaN)
 #pragma unroll
-    for (int i = 1; i < N; ++i) g = fmaxf(g, x[j][i]);
-    g = lanes_reduce<kSampleGroup / N>(g, [](float a, float b) { return fmaxf(a, b); });
+    for (int i = 0; i < N; ++i) g[j] = quiet_max(g[j], x[j][i]);
+  }
+  group_max(g);
+#pragma unroll
+  for (int j = 0; j < L; ++j) {
     const int gi = seg * (kSampleSeg / kSampleGroup) + (j * kSampleScan + tid) * N / kSampleGroup;
-    if (lane % (kSampleGroup / N) == 0 && gi < A.groups) A.gmax[(int64_t)r * A.groups + gi] = g;
-    m = fmaxf(m, g);
+    if (lane % (kSampleGroup / N) == 0 && gi < A.groups) A.gmax[(int64_t)r * A.groups + gi] = g[j];
+    m = quiet_max(m, g[j]);
   }
   m = wave_max(m);
   if (lane == 0) s_max[wave] = m;
@@ -234,17 +297,27 @@ __global__ __launch_bounds__(kSampleScan) void sample_scan_kernel(SampleArgs A) 
   for (int i = 1; i < kSampleScan / 64; ++i) m = fmaxf(m, s_max[i]);
   const int64_t at = (int64_t)r * A.segs + seg;
   if (tid == 0) A.smax[at] = m;
+  // ids below the last bin with mass go to the one after it, and so does NaN
+  const SampleGrid grid(m, p, kSampleGrid);
+  const float bottom = (float)((double)(grid.top - (kSampleBins - 1)) * p.step);
+  // the bin of an id and its weight relative to the bin's middle
+  double whole = SampleGrid::kInt;
+  asm("" : "+s"(whole));
+  auto place = [&](const BinWeight& weight, float l, int& d) {
+    const double x = (double)quiet_max(l, bottom), t = fma(x, p.c64, whole);
+    d = grid.top - (int)__double_as_longlong(t);
+    return weight(fma(x, p.c64, whole - t));
+  };
   if (mode == kScanMass) {
     double s = 0.0;
-    const float top = floorf(m * p.cb);
-    if (fabsf(top) < kSampleGrid) {                // (uniform)
+    if (grid.on) {                                 // (uniform)
       // exp((l - m) / T) as the factor of the logit's bin, from a table, and
-      // the six terms of its place in the bin
+      // the five terms of its place in the bin
       double* factor = (double*)s_hist;
       for (int i = tid; i < kSampleBins; i += kSampleScan)
-        factor[i] = i < kSampleBins - 1 ? exp_bins(fma((double)m, -p.c64, (double)top - (double)i + 1.0)) : 0.0;
+        factor[i] = i < kSampleBins - 1 ? exp_bins(fma((double)m, -p.c64, (double)(grid.top - i))) : 0.0;
       __syncthreads();
-      const EdgeWeight weight;
+      const BinWeight weight;
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
@@ -254,10 +327,9 @@ __global__ __launch_bounds__(kSampleScan) void sample_scan_kernel(SampleArgs A) 
           double w[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float b = floorf(x[j][q + i] * p.cb), d = top - b;
-            const double e = weight(fma((double)x[j][q + i], p.c64, -(double)(b + 1.f)));
-            const bool in = d < (float)(kSampleBins - 1);   // false for -inf
-            w[i] = in ? e * factor[in ? (int)d : 0] : 0.0;
+            int d;
+            w[i] = place(weight, x[j][q + i], d);
+            w[i] *= factor[d];
           }
           s += w[0] + w[1];
           asm volatile("" : "+v"(s));
@@ -277,30 +349,27 @@ __global__ __launch_bounds__(kSampleScan) void sample_scan_kernel(SampleArgs A) 
       A.smass[at] = s;
     }
   } else if (mode == kScanHist && A.hist) {
-    const float top = floorf(m * p.cb);
     int last = -1;
-    if (fabsf(top) < kSampleGrid) {                // false for -inf and NaN
+    if (grid.on) {
       const double scale = sample_scale(A.V);
-      const EdgeWeight weight;
+      const BinWeight weight;
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
         for (int q = 0; q < N; q += 4) {
           // four ids at a time: their polynomials interleave
-          float d[4];
+          int d[4];
           uint64_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float b = floorf(x[j][q + i] * p.cb);
-            d[i] = top - b;
-            w[i] = sample_units(weight(fma((double)x[j][q + i], p.c64, -(double)(b + 1.f))), scale);
+            w[i] = sample_units(place(weight, x[j][q + i], d[i]), scale);
             asm volatile("" : "+v"(w[i]), "+v"(d[i]));
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (d[i] < (float)(kSampleBins - 1)) { // false for -inf
-              atomicAdd(&s_hist[(int)d[i]], (unsigned long long)w[i]);
-              last = max(last, (int)d[i]);
+            if (d[i] < kSampleBins - 1) {
+              atomicAdd(&s_hist[d[i]], (unsigned long long)w[i]);
+              last = max(last, d[i]);
             }
         }
     }
@@ -425,20 +494,22 @@ struct SamplePicker {
   const SampleRow p;
   const T* row;
   const float* gmax;
-  float m, top;                // the largest logit and its bin on the grid
-  bool grid;                   // bins lie on the scan's grid
+  float m;                     // the largest logit
+  SampleGrid grid;             // on: bins are the scan's
   double scale;
 
   __device__ explicit SamplePicker(const SampleArgs& a)
       : A(a), s(sample_shared()), r(blockIdx.x), p(sample_row(a, blockIdx.x)), row((const T*)a.z + (int64_t)blockIdx.x * a.ldz),
-        gmax(a.gmax + (int64_t)blockIdx.x * a.groups), scale(sample_scale(a.V)) {}
+        gmax(a.gmax + (int64_t)blockIdx.x * a.groups), grid(INFINITY, p, 0.0), scale(sample_scale(a.V)) {}
 
   // Bin of a logit below the largest: non-decreasing as l falls.  The last
   // bin has no mass.
   __device__ __forceinline__ int bin(float l) const {
-    const float x = grid ? top - floorf(l * p.cb) : (m - l) * p.cb;
-    const int b = (int)fminf(x, (float)(kSampleBins - 1));   // NaN (inf * 0): the last bin
-    return l == m ? 0 : (l == -INFINITY ? kSampleBins - 1 : b);
+    if (l == m) return 0;
+    const float x = (m - l) * p.cb;
+    const float y = fminf(x, (float)(kSampleBins - 1));      // NaN (inf * 0): the last bin
+    // (a logit two bins past the last one is not formed on the grid, where it could leave 32 bits)
+    return grid.on && x < (float)(kSampleBins + 1) ? min(grid.top - grid.at(l), kSampleBins - 1) : (int)y;
   }
   __device__ __forceinline__ uint64_t mass(float l) const {
     return sample_units(sample_weight(l, m, p.c64), scale);
@@ -549,16 +620,18 @@ struct SamplePicker {
     const int ng = s.n2;
     if (ng > most) return kSampleList + 1;
     const int lane = threadIdx.x & 63;
-    for (int g0 = (threadIdx.x >> 6) * 4; g0 < ng; g0 += 4 * (kSamplePick / 64)) {
-      float x[4];
-      int v[4];
+    constexpr int D = 8;                           // groups per wave in flight
+    constexpr int W = kSamplePick / 64;
+    for (int g0 = threadIdx.x >> 6; g0 < ng; g0 += D * W) {
+      float x[D];
+      int v[D];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = g0 + j < ng ? list[g0 + j] * kSampleGroup + lane : A.V;
+      for (int j = 0; j < D; ++j) {
+        v[j] = g0 + j * W < ng ? list[g0 + j * W] * kSampleGroup + lane : A.V;
         x[j] = v[j] < A.V ? sample_logit(load_elem<E>(row + v[j])) : -INFINITY;
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < D; ++j)
         if (v[j] < A.V && bin(x[j]) <= b) {
           const int at = atomicAdd(&s.n, 1);
           if (at < kSampleList) s.key[at] = cand_key(x[j], (uint32_t)v[j]);
@@ -594,6 +667,7 @@ struct SamplePicker {
     if (i < n) {
       int c = 0;
       uint64_t a = 0;
+#pragma unroll 4
       for (int j = q; j < n; j += Q)
         if (s.key[j] > k) {
           ++c;
@@ -617,6 +691,7 @@ struct SamplePicker {
     const uint64_t total = block_total(s, q == 0 && keep ? w : (uint64_t)0);   // its barriers order the writes
     if (keep) {
       uint64_t a = 0;
+#pragma unroll 4
       for (int j = q; j < n; j += Q)
         if ((uint32_t)s.key[j] >= (uint32_t)k) a += wt[j];       // ids <= this one
       atomicAdd((unsigned long long*)&pre[i], (unsigned long long)a);
@@ -672,18 +747,17 @@ struct SamplePicker {
 
   // ---- flat rows, from the scan's histograms -------------------------------
   // Mass of bin j of the row relative to the largest logit: its entries are
-  // kept relative to the bin's upper edge, top - j + 1 on the grid.
+  // kept relative to the bin's middle, top - j on the grid.
   __device__ __forceinline__ double bin_factor(int j) const {
-    return exp_bins(fma((double)m, -p.c64, (double)top - (double)j + 1.0));
+    return exp_bins(fma((double)m, -p.c64, (double)(grid.top - j)));
   }
   __device__ __forceinline__ int seg_offset(int sg) const {
     // bins between the row's largest logit and the segment's
-    const float b = top - floorf(A.smax[(int64_t)r * A.segs + sg] * p.cb);
-    return (int)fminf(b, (float)kSampleBins);      // -inf: outside
+    return bin(A.smax[(int64_t)r * A.segs + sg]);  // -inf: the last one
   }
 
-  // The kept set: every id with l cb >= edge and, below it, those that are
-  // not after the id `last` with the logit `least` in descending order.
+  // The kept set: every id with l >= edge (NaN: none) and, below it, those that
+  // are not after the id `last` with the logit `least` in descending order.
   struct Kept {
     float edge, least;
     int last;
@@ -694,7 +768,7 @@ struct SamplePicker {
     return lim == ~0ull ? Kept{edge, INFINITY, -1} : Kept{edge, key_logit(lim), key_id(lim)};
   }
   __device__ __forceinline__ bool is_kept(const Kept& k, int v, float l) const {
-    return l * p.cb >= k.edge || l > k.least || (l == k.least && v <= k.last);
+    return l >= k.edge || l > k.least || (l == k.least && v <= k.last);
   }
 
   // Draw, given the segments' kept masses in s.bins.  A segment whose mass
@@ -747,8 +821,10 @@ struct SamplePicker {
   }
 
   // top_p and min_p without top_k: the row's histogram into s.bins; returns
-  // the mass of the row, and the bins lo .. hi that the kept set ends in.
-  __device__ __forceinline__ double join_hist(int& lo, int& hi) {
+  // the mass of the row, the bins lo .. hi that the kept set ends in, and about
+  // how many ids lie in the bins up to hi (each has a mass within a hundredth
+  // of one unit of its bin's).
+  __device__ __forceinline__ double join_hist(int& lo, int& hi, double& ids) {
     const int64_t at0 = (int64_t)r * A.segs;
     double* bm = (double*)s.bins;
     // per segment: where its histogram starts among the row's bins, its length
@@ -786,6 +862,7 @@ struct SamplePicker {
       lo = min(lo, jb);
       hi = min(hi, jb);
     }
+    ids = block_total(s, (j0 <= hi ? (double)a0 : 0.0) + (j1 <= hi ? (double)a1 : 0.0)) / scale;
     return all;
   }
 
@@ -795,14 +872,16 @@ struct SamplePicker {
     const int64_t at0 = (int64_t)r * A.segs;
     const double* bm = (const double*)s.bins;
     const double need = p.top_p * all;
-    // the border's ids: on the grid, bins lo .. hi are lb <= l cb < ub
+    // the border's ids, bins lo .. hi: lb <= l < ub
     if (threadIdx.x == 0) s.n = s.n2 = 0;
     for (int i = threadIdx.x; i < kSampleSub; i += kSamplePick) s.sub[i] = 0;
     double part = 0.0;
     for (int j = threadIdx.x; j < lo; j += kSamplePick) part += bm[j];
     const double above = block_total(s, part);     // (orders the writes above)
-    const float lb = top - (float)hi, ub = top - (float)lo + 1.f;
-    const float per = (float)kSampleSub / (float)(hi - lo + 1);
+    const float lb = grid.least(hi, p.step), ub = lo > 0 ? grid.least(lo - 1, p.step) : INFINITY;
+    // parts of the border, in the logits' order
+    const float per = (float)kSampleSub / (float)(hi - lo + 1), first = (float)(grid.top - lo) + 0.5f;
+    auto part_of = [&](float l) { return min(max((int)((first - l * p.cb) * per), 0), kSampleSub - 1); };
     // 32 ids per thread and step: a bit each for those in the border, whose
     // ids then go to the list (hardly any lane has more than two)
     constexpr int D = 32 / N;
@@ -825,8 +904,7 @@ struct SamplePicker {
           float l;
           if constexpr (N == 8) l = __uint_as_float((i & 1) ? (u[j][i >> 1] & 0xffff0000u) : (u[j][i >> 1] << 16));
           else l = __uint_as_float(u[j][i]);
-          const float t = l * p.cb;
-          hits |= t >= lb && t < ub ? 1u << (j * N + i) : 0u;
+          hits |= l >= lb && l < ub ? 1u << (j * N + i) : 0u;
         }
       while (hits) {
         const int q = __builtin_ctz(hits);
@@ -838,8 +916,8 @@ struct SamplePicker {
     // the last vector, where it crosses the row's end
     if (threadIdx.x < A.V % N) {
       const int v = A.V - A.V % N + (int)threadIdx.x;
-      const float t = load_elem<E>(row + v) * p.cb;
-      if (t >= lb && t < ub) {
+      const float l = load_elem<E>(row + v);
+      if (l >= lb && l < ub) {
         const int at = atomicAdd(&s.n, 1);
         if (at < kSampleList) ids[at] = v;
       }
@@ -865,7 +943,7 @@ struct SamplePicker {
       s.key[i] = key[j];
       if (p.top_p < 1.0) {
         const float l = key_logit(key[j]);
-        atomicAdd((unsigned long long*)&s.sub[min((int)((ub - l * p.cb) * per), kSampleSub - 1)], (unsigned long long)mass(l));
+        atomicAdd((unsigned long long*)&s.sub[part_of(l)], (unsigned long long)mass(l));
       }
     }
     __syncthreads();
@@ -881,10 +959,8 @@ struct SamplePicker {
         uint64_t before;
         const int sb = block_find(s, kSampleSub, want, [&](int i) { return s.sub[i]; }, before);
         if (sb >= 0) {
-          for (int i = threadIdx.x; i < n; i += kSamplePick) {
-            const float t = key_logit(s.key[i]) * p.cb;
-            if (min((int)((ub - t) * per), kSampleSub - 1) == sb) s.aux[atomicAdd(&s.n2, 1)] = s.key[i];
-          }
+          for (int i = threadIdx.x; i < n; i += kSamplePick)
+            if (part_of(key_logit(s.key[i])) == sb) s.aux[atomicAdd(&s.n2, 1)] = s.key[i];
           __syncthreads();
           const int ns = s.n2;
           __syncthreads();
@@ -1004,7 +1080,7 @@ struct SamplePicker {
     if (p.top_k > 0) lim = cut<false>(lim, [&](uint64_t) { return (uint64_t)p.top_k; });
     if (p.top_p < 1.0)
       lim = cut<true>(lim, [&](uint64_t total) { return (uint64_t)fmax(ceil(p.top_p * (double)total), 1.0); });
-    const Kept k = kept_from(INFINITY, lim);
+    const Kept k = kept_from(NAN, lim);
     for (int i = threadIdx.x; i < A.segs; i += kSamplePick) s.bins[i] = 0;
     __syncthreads();
     // a wave's ids of one vector lie in one segment (64 * N divides it)
@@ -1024,8 +1100,7 @@ struct SamplePicker {
 
   __device__ __forceinline__ void set_max(float largest) {
     m = largest;
-    top = floorf(m * p.cb);
-    grid = fabsf(top) < kSampleGrid - 2 * kSampleBins;
+    grid = SampleGrid(m, p, kSampleGrid - 2 * kSampleBins);
   }
 
   __device__ __forceinline__ void pick() {
@@ -1043,7 +1118,7 @@ struct SamplePicker {
     if (p.greedy) return pick_greedy();
     set_max(m);
     const int mode = sample_scan_mode(A, p);
-    Kept k = kept_from(INFINITY, 0);
+    Kept k = kept_from(NAN, 0);
     if (mode == kScanMass) {
       for (int i = threadIdx.x; i < A.segs; i += kSamplePick) {
         const double v = A.smass[(int64_t)r * A.segs + i];
@@ -1053,18 +1128,19 @@ struct SamplePicker {
     } else {
       // how deep the kept ids can lie
       const bool hist = mode == kScanHist && A.hist;
-      if (hist && !grid) return sample_stream_row<E>(A, m);
-      double all = 0.0;
+      if (hist && !grid.on) return sample_stream_row<E>(A, m);
+      double all = 0.0, ids = 0.0;
       int lo = 0, hi = kSampleBins - 2;
-      if (hist) all = join_hist(lo, hi);
+      if (hist) all = join_hist(lo, hi, ids);
       else if (p.top_k > 0) hi = group_bin(p.top_k);
       // (top_p of top_k's ids needs the mass of all of them)
       if (!hist && p.min_p > 0.0 && p.top_p == 1.0)
         hi = min(hi, (int)fmin(-64.0 * log(p.min_p) + 3.0, (double)(kSampleBins - 2)));
-      // (a histogram's row takes the list only if it can be ranked at once:
-      // longer lists cost more than the border's ids alone)
-      const int n = gather(hi, hist ? kSampleRank : kSampleList);
-      if (n <= (hist ? kSampleRank : kSampleList)) {
+      // (a histogram's row takes the list only if it is short: 250 ids cost
+      // more than the border's ids alone, 23 us against 21 in one row)
+      const int most = hist ? (ids <= 0.75 * kSampleRank ? kSampleRank : 0) : kSampleList;
+      const int n = gather(hi, most);
+      if (n <= most) {
         if (!hist && p.top_k == 0 && p.top_p < 1.0) {
           uint64_t part = 0;
           for (int i = threadIdx.x; i < n; i += kSamplePick) part += mass(key_logit(s.key[i]));

@@ -412,6 +412,41 @@ def test_sample_long_ties(V, value):
             _check_sample(z.cuda(), torch.full((3,), u, device="cuda:0"), kw)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_sample_logits_on_an_even_grid(dtype):
+    """Logits whose distances from the largest are whole and half multiples of
+    T/64, and their fp32 neighbours; rows long enough for every path."""
+    torch = _t()
+    g = torch.Generator().manual_seed(5)
+    V = 40000
+    z = torch.stack([torch.randint(-n, n, (V,), generator=g).float() / 128 for n in (60, 400, 1500, 3000)])
+    if dtype == "float32":
+        near = torch.randint(-1, 2, z.shape, generator=g)
+        z = torch.where(near > 0, torch.nextafter(z, torch.full_like(z, 99.0)),
+                        torch.where(near < 0, torch.nextafter(z, torch.full_like(z, -99.0)), z))
+    z = z.to(getattr(torch, dtype)).cuda()
+    for kw in (dict(), dict(top_p=0.3), dict(top_p=0.9), dict(min_p=0.2), dict(top_p=0.95, min_p=0.01), dict(temperature=0.5, top_p=0.8),
+               dict(temperature=2.0, min_p=0.5), dict(top_k=300), dict(top_k=9000, top_p=0.5)):
+        log(f"[sample grid] {dtype} {kw}")
+        _check_sample(z, torch.rand(4, generator=g).cuda(), kw)
+
+
+def test_sample_infinities_in_long_rows():
+    torch = _t()
+    V = 30000
+    z = torch.randn(4, V, generator=torch.Generator().manual_seed(8))
+    z[0, 77::1000] = float("inf")
+    z[1] = torch.finfo(torch.float32).min
+    z[1, 500:9000] = torch.linspace(-3, 3, 8500)
+    z[2, 20000:] = float("nan")
+    z[3, :29999] = -float("inf")
+    z = z.cuda()
+    for u in (0.0, 0.4, 0.95):
+        for kw in (dict(), dict(top_k=2), dict(top_k=5000), dict(top_p=0.3), dict(top_p=0.9, min_p=0.1), dict(top_k=7000, top_p=0.6)):
+            log(f"[sample inf] u={u} {kw}")
+            _check_sample(z, torch.full((4,), u, device="cuda:0"), kw)
+
+
 def test_sample_per_row_parameters_and_large_rows():
     torch = _t()
     g = torch.Generator().manual_seed(77)
