@@ -28,7 +28,7 @@ constexpr int64_t kNormMaxBlocks = 1 << 20;   // forward: rows past it are taken
 
 template <class T, class WT, int WPR, int NV>
 int32_t norm_fwd_launch(const NormFwdArgs& A, hipStream_t st) {
-  typedef NormCfg<WPR> C;
+  typedef NormFwdCfg<WPR> C;
   const dim3 grid((unsigned)std::min<int64_t>(cdiv(A.T, C::kRows), kNormMaxBlocks));
   if (A.q) hipLaunchKernelGGL((norm_fwd_kernel<T, WT, WPR, NV, true>), grid, dim3(C::kThreads), 0, st, A);
   else hipLaunchKernelGGL((norm_fwd_kernel<T, WT, WPR, NV, false>), grid, dim3(C::kThreads), 0, st, A);
@@ -37,7 +37,7 @@ int32_t norm_fwd_launch(const NormFwdArgs& A, hipStream_t st) {
 }
 template <class T, class WT, int WPR, int NV>
 int32_t norm_bwd_launch(const NormBwdArgs& A, hipStream_t st) {
-  typedef NormCfg<WPR> C;
+  typedef NormBwdCfg<WPR> C;
   const dim3 grid((unsigned)norm_bwd_blocks(A.T, A.d));
   if (A.q) hipLaunchKernelGGL((norm_bwd_kernel<T, WT, WPR, NV, true>), grid, dim3(C::kThreads), 0, st, A);
   else hipLaunchKernelGGL((norm_bwd_kernel<T, WT, WPR, NV, false>), grid, dim3(C::kThreads), 0, st, A);
@@ -48,7 +48,7 @@ int32_t norm_bwd_launch(const NormBwdArgs& A, hipStream_t st) {
 // The narrowest variant that holds a row: NV vectors of 8 elements per lane,
 // WPR waves per row.  The backward spreads rows wider than 1024 over two waves
 // and more: its accumulators take as many registers as two rows, and with one
-// wave per row of 2880 they left room for two waves per SIMD (128K rows of 2880 from 8 bits: 527 us, with two waves 415).
+// wave per row of 2880 they left room for two waves per SIMD (128K rows of 2880 from 8 bits: 527 us, with two waves 464 at once and 407 since).
 template <class T, class WT>
 int32_t norm_fwd(const NormFwdArgs& A, hipStream_t st) {
   if (A.d <= 512) return norm_fwd_launch<T, WT, 1, 1>(A, st);

@@ -15,7 +15,7 @@
 // the backward's up to 1024 elements): all reductions are lane exchanges, no
 // barrier; wider rows are spread over two to sixteen waves.  131072 bf16 rows
 // of 2880 with checkpoints in 8 bits: forward 351 us (1.91 GB, 5.4 TB/s),
-// backward 415 us (1.91 GB, 4.6 TB/s) and 8 us for the partial rows, where a
+// backward 407 us (1.91 GB, 4.7 TB/s) and 5 us for the partial rows, where a
 // copy of gigabytes reaches 4.7 (read and write counted); 8192 rows without
 // checkpoints 22 and 31 us, what of them the caches hold included.
 //
@@ -31,12 +31,16 @@
 
 namespace kd {
 
-// Rows per block of threads and its size: four waves, or one row of sixteen.
-template <int WPR> struct NormCfg {
-  static constexpr int kRows = WPR < 4 ? 4 / WPR : 1;
+// Rows per block of threads and its size: WAVES waves (four in the forward;
+// eight in the backward, whose blocks write a partial row each), or one row of
+// more.
+template <int WPR, int WAVES> struct NormCfg {
+  static constexpr int kRows = WPR < WAVES ? WAVES / WPR : 1;
   static constexpr int kWaves = WPR * kRows;
   static constexpr int kThreads = 64 * kWaves;
 };
+template <int WPR> using NormFwdCfg = NormCfg<WPR, 4>;
+template <int WPR> using NormBwdCfg = NormCfg<WPR, 8>;
 
 // Statistics over a row spread over WPR waves: sums, left in every lane.
 // s_red: one float2 per wave of the block, rewritten per call (the caller's
@@ -121,9 +125,9 @@ struct NormFwdArgs {
 };
 
 template <class T, class WT, int WPR, int NV, bool CKPT>
-__global__ __launch_bounds__(NormCfg<WPR>::kThreads) void norm_fwd_kernel(NormFwdArgs A) {
-  __shared__ float2 s_red[2][NormCfg<WPR>::kWaves];
-  constexpr int R = NormCfg<WPR>::kRows;
+__global__ __launch_bounds__(NormFwdCfg<WPR>::kThreads) void norm_fwd_kernel(NormFwdArgs A) {
+  __shared__ float2 s_red[2][NormFwdCfg<WPR>::kWaves];
+  constexpr int R = NormFwdCfg<WPR>::kRows;
   static_assert(WPR == 1 || R == 1, "rows of one block advance together");
   const NormCols<WPR, NV> C(A.d);
   const int wave = threadIdx.x >> 6, d = A.d;
@@ -223,10 +227,10 @@ template <int WPR, int NV> constexpr bool norm_hold() { return WPR * NV < 64; }
 
 // Blocks of rows in turn: block b takes rows b, b + grid, ... (times kRows).
 template <class T, class WT, int WPR, int NV, bool CKPT>
-__global__ __launch_bounds__(NormCfg<WPR>::kThreads, (sizeof(T) == 2 && sizeof(WT) == 2 && NV < 4 ? 4 : 1))
+__global__ __launch_bounds__(NormBwdCfg<WPR>::kThreads, (sizeof(T) == 2 && sizeof(WT) == 2 && NV < 4 ? 4 : 1))
 void norm_bwd_kernel(NormBwdArgs A) {
   typedef typename std::conditional<CKPT, int8_t, T>::type XT;
-  typedef NormCfg<WPR> Cfg;
+  typedef NormBwdCfg<WPR> Cfg;
   constexpr bool HOLD = norm_hold<WPR, NV>();
   constexpr int R = Cfg::kRows;
   __shared__ float2 s_red[2][Cfg::kWaves];

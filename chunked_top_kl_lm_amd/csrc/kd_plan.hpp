@@ -240,15 +240,15 @@ inline int32_t make_cache_plan(int64_t T, int64_t d, int64_t V, int64_t K, int64
 // Operators around the head (see kd_norm.hpp, kd_logits.hpp, kd_sample.hpp)
 // ---------------------------------------------------------------------------
 
-// Layer norm backward: blocks of four waves (eight or sixteen for rows wider
-// than 8192), one partial weight-gradient row each.  Up to a block per CU as long
-// as there are rows; past that a block takes at least eight, so that the
-// partial rows stay a small part of the traffic, up to the blocks that run at
-// once (four per CU; two for 4097 .. 8192, one of the wider).
+// Layer norm backward: blocks of eight waves (sixteen for rows of 8193 ..
+// 16384), one partial weight-gradient row each.  A block per CU as long as
+// there are rows for it; as many as run at once (two per CU, one of rows wider
+// than 4096) from sixteen rows per block of these on, so that the partial rows
+// stay a small part of the traffic.
 inline int64_t norm_bwd_blocks(int64_t T, int64_t d) {
-  const int64_t rows = d <= 1024 ? 4 : d <= 6 * 512 ? 2 : 1;   // rows in flight per block
-  const int64_t most = (d <= 4096 ? 4 : d <= 8192 ? 2 : 1) * kNumCU;
-  return std::max<int64_t>(std::min<int64_t>(kNumCU, cdiv(T, rows)), std::min<int64_t>(most, T / 8));
+  const int64_t rows = d <= 1024 ? 8 : d <= 6 * 512 ? 4 : d <= 8192 ? 2 : 1;   // rows in flight per block
+  if (T <= 16 * kNumCU || d > 4096) return std::min<int64_t>(kNumCU, cdiv(T, rows));
+  return 2 * kNumCU;
 }
 inline size_t norm_bwd_workspace(int64_t T, int64_t d) {
   return align256((size_t)norm_bwd_blocks(T, d) * 2 * (size_t)d * sizeof(float));
