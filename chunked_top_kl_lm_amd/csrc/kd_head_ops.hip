@@ -49,7 +49,7 @@ int32_t norm_bwd_launch(const NormBwdArgs& A, hipStream_t st) {
 // WPR waves per row.  The backward spreads rows wider than 1024 over two waves
 // and more: its accumulators take as many registers as two rows, and with one
 // wave per row of 2880 they left room for two waves per SIMD (128K rows of 2880
-// from 8 bits: 527 us; with two waves 464 at once and 407 since).
+// from 8 bits: 527 us; with two waves 464 at once and 402 since).
 template <class T, class WT>
 int32_t norm_fwd(const NormFwdArgs& A, hipStream_t st) {
   if (A.d <= 512) return norm_fwd_launch<T, WT, 1, 1>(A, st);

@@ -15,7 +15,7 @@
 // the backward's up to 1024 elements): all reductions are lane exchanges, no
 // barrier; wider rows are spread over two to sixteen waves.  131072 bf16 rows
 // of 2880 with checkpoints in 8 bits: forward 351 us (1.91 GB, 5.4 TB/s),
-// backward 407 us (1.91 GB, 4.7 TB/s) and 5 us for the partial rows, where a
+// backward 402 us (1.91 GB, 4.7 TB/s) and 5 us for the partial rows, where a
 // copy of gigabytes reaches 4.7 (read and write counted); 8192 rows without
 // checkpoints 22 and 31 us, what of them the caches hold included.
 //
