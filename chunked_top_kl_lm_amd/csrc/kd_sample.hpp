@@ -286,6 +286,9 @@ __global__ __launch_bounds__(kSampleScan) void sample_scan_kernel(SampleArgs A) 
     if (lane % (kSampleGroup / N) == 0 && gi < A.groups) A.gmax[(int64_t)r * A.groups + gi] = g[j];
     m = quiet_max(m, g[j]);
   }
+  // (the compiler, which keeps a lane-crossing read two instructions behind its
+  // operand's last write, does not see the one in quiet_max)
+  asm("s_nop 1" : "+v"(m));
   m = wave_max(m);
   if (lane == 0) s_max[wave] = m;
   if (mode == kScanHist && A.hist)
